@@ -20,6 +20,7 @@ _lock = threading.Lock()
 
 SV_OK, SV_ERR_INVALID_ARG, SV_ERR_UNSUPPORTED, SV_ERR_CUDA, SV_ERR_TIMEOUT = range(5)
 SV_BF16, SV_F32 = 0, 1
+SV_MXFP8, SV_MXFP4, SV_NVFP4 = range(3)
 SV_OP_LINATTN_FWD, SV_OP_BLOCK_STATE_UPDATE, SV_OP_BLOCK_CAUSAL_ATTN, SV_OP_CACHE_STEP = range(4)
 
 #: every symbol include/svlinattn.h declares
@@ -27,7 +28,8 @@ EXPORTS = (
     "sv_workspace_bytes", "sv_workspace_init", "sv_device_status", "sv_workspace_set_mirror", "sv_linattn_fwd",
     "sv_block_state_update", "sv_block_causal_attn", "sv_cache_step", "sv_cache_step_noalloc",
     "sv_cache_step_noalloc_status", "sv_temporal_conv", "sv_temporal_conv_step", "sv_qkv_projection",
-    "sv_out_projection", "sv_rope3d_table_bytes", "sv_rope3d_table", "sv_block_causal_attn_rope", "sv_profile_events",
+    "sv_out_projection", "sv_mx_code_bytes", "sv_mx_scale_bytes", "sv_mx_global_scale", "sv_mx_quantize",
+    "sv_mx_dequantize", "sv_rmsnorm", "sv_mx_projection", "sv_mx_qkv_projection", "sv_rope3d_table_bytes", "sv_rope3d_table", "sv_block_causal_attn_rope", "sv_profile_events",
     "sv_last_error", "sv_selftest_wait_timeout", "sv_version",
 )
 
@@ -38,6 +40,13 @@ class SvRope3d(ctypes.Structure):
     _fields_ = [("table", ctypes.c_void_p), ("frames", ctypes.c_int), ("height", ctypes.c_int),
                 ("width", ctypes.c_int), ("D", ctypes.c_int), ("pairs_t", ctypes.c_int), ("pairs_h", ctypes.c_int),
                 ("pairs_w", ctypes.c_int), ("frame0", ctypes.c_int)]
+
+
+class SvMx(ctypes.Structure):
+    """The C descriptor sv_mx (include/svlinattn.h)."""
+
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("gscale", ctypes.c_void_p),
+                ("rows", ctypes.c_longlong), ("cols", ctypes.c_int), ("fmt", ctypes.c_int)]
 
 
 class SvError(RuntimeError):
@@ -90,6 +99,23 @@ def load() -> ctypes.CDLL:
         lib.sv_qkv_projection.restype = i
         lib.sv_out_projection.argtypes = [vp, vp, vp, i, i, i, i, i, vp, sz, vp]
         lib.sv_out_projection.restype = i
+        ll, mx = ctypes.c_longlong, ctypes.POINTER(SvMx)
+        lib.sv_mx_code_bytes.argtypes = [i, ll, i]
+        lib.sv_mx_code_bytes.restype = sz
+        lib.sv_mx_scale_bytes.argtypes = [i, ll, i]
+        lib.sv_mx_scale_bytes.restype = sz
+        lib.sv_mx_global_scale.argtypes = [vp, ll, i, vp, vp]
+        lib.sv_mx_global_scale.restype = i
+        lib.sv_mx_quantize.argtypes = [vp, i, i, i, i, i, mx, vp]
+        lib.sv_mx_quantize.restype = i
+        lib.sv_mx_dequantize.argtypes = [mx, vp, i, vp]
+        lib.sv_mx_dequantize.restype = i
+        lib.sv_rmsnorm.argtypes = [vp, vp, vp, vp, ll, i, i, f, vp, mx, vp]
+        lib.sv_rmsnorm.restype = i
+        lib.sv_mx_projection.argtypes = [mx, mx, vp, vp, sz, vp]
+        lib.sv_mx_projection.restype = i
+        lib.sv_mx_qkv_projection.argtypes = [mx, mx, vp, vp, vp, i, i, i, i, vp, sz, vp]
+        lib.sv_mx_qkv_projection.restype = i
         lib.sv_rope3d_table_bytes.argtypes = [i, i, i, i]
         lib.sv_rope3d_table_bytes.restype = sz
         lib.sv_rope3d_table.argtypes = [vp, sz, i, i, i, i, i, i, i, f, vp]
@@ -434,3 +460,204 @@ def sv_block_causal_attn_rope(q, k, v, block_len: int, rope: Rope3dTable, frame0
                                             eps, _ptr(S_in), _ptr(z_in), _ptr(S_out), _ptr(z_out), ctypes.byref(d),
                                             ws.ptr, ws.nbytes, _stream(stream)))
     return o
+
+
+_MX_BLOCK = {SV_MXFP8: 32, SV_MXFP4: 32, SV_NVFP4: 16}
+_MX_RUN = {SV_MXFP8: 128, SV_MXFP4: 256, SV_NVFP4: 256}  # columns in 128 bytes of codes
+
+
+class MxTensor:
+    """A microscaled matrix [rows, cols] (formats and layout: include/svlinattn.h).
+
+    codes: uint8 [rows, cols] (SV_MXFP8) or [rows, cols / 2]; scales: uint8 [row tiles, block tiles, 32, 4, 4];
+    gscale: float32 [1], the tensor scale of SV_NVFP4, None for the other formats. The tensors are read
+    at every call: change them in place, or make another MxTensor.
+    """
+
+    __slots__ = ("codes", "scales", "gscale", "rows", "cols", "fmt", "_c", "_ref")
+
+    def __init__(self, codes, scales, rows: int, cols: int, fmt: int, gscale=None):
+        if fmt not in _MX_BLOCK:
+            raise ValueError("fmt must be SV_MXFP8, SV_MXFP4 or SV_NVFP4")
+        if rows < 1 or cols < 32 or cols % 32 != 0:
+            raise ValueError("rows must be >= 1 and cols a positive multiple of 32")
+        dev = codes.device
+        if not codes.is_cuda:
+            raise ValueError("codes must live on a CUDA device")
+        if codes.dtype != torch.uint8 or codes.shape != (rows, cols if fmt == SV_MXFP8 else cols // 2) or not codes.is_contiguous():
+            raise ValueError("codes must be a contiguous uint8 tensor [rows, cols] (SV_MXFP8) or [rows, cols / 2]")
+        if (scales.dtype != torch.uint8 or scales.shape != _mx_scale_shape(rows, cols, fmt) or not scales.is_contiguous()
+                or scales.device != dev):
+            raise ValueError(f"scales must be a contiguous uint8 tensor {_mx_scale_shape(rows, cols, fmt)} on codes' device")
+        if (gscale is None) != (fmt != SV_NVFP4):
+            raise ValueError("SV_NVFP4 needs a tensor scale gscale; the other formats take none")
+        if gscale is not None and (gscale.dtype != torch.float32 or gscale.numel() != 1 or gscale.device != dev):
+            raise ValueError("gscale must be a float32 tensor of one value on codes' device")
+        self.codes, self.scales, self.gscale = codes, scales, gscale
+        self.rows, self.cols, self.fmt = rows, cols, fmt
+        self._c = SvMx(codes.data_ptr(), scales.data_ptr(), None if gscale is None else gscale.data_ptr(), rows, cols, fmt)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, fmt: int, gscale=None, device=None):
+        """An MxTensor with uninitialised codes and scales (an output for sv_mx_quantize or sv_rmsnorm)."""
+        if fmt not in _MX_BLOCK:
+            raise ValueError("fmt must be SV_MXFP8, SV_MXFP4 or SV_NVFP4")
+        device = device if device is not None else (gscale.device if gscale is not None else torch.device("cuda"))
+        codes = torch.empty((rows, cols if fmt == SV_MXFP8 else cols // 2), dtype=torch.uint8, device=device)
+        scales = torch.empty(_mx_scale_shape(rows, cols, fmt), dtype=torch.uint8, device=device)
+        return cls(codes, scales, rows, cols, fmt, gscale)
+
+    @property
+    def device(self):
+        return self.codes.device
+
+
+def _mx_scale_shape(rows, cols, fmt):
+    run = _MX_RUN[fmt]
+    return (-(-rows // 128), -(-cols // run) * (run // _MX_BLOCK[fmt]) // 4, 32, 4, 4)
+
+
+def _on_device(t):
+    """Makes t's device current for the call when it is not (a no-op context otherwise)."""
+    return torch.cuda.device(t.device)
+
+
+def _mx_out(out, rows, cols, fmt, gscale, device):
+    if out is None:
+        return MxTensor.empty(rows, cols, fmt, gscale, device)
+    if out.rows != rows or out.cols != cols or out.fmt != fmt or out.device != device:
+        raise ValueError(f"out must be a microscaled [{rows}, {cols}] matrix of the call's format on x's device")
+    if gscale is not None and gscale is not out.gscale:
+        raise ValueError("gscale must be out's own tensor scale, or None")
+    return out
+
+
+def _dense(x, name):
+    if not x.is_cuda or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+
+
+def sv_mx_global_scale(x, g=None, stream=None):
+    """The tensor scale of SV_NVFP4: max |x| / (6 * 448) as a float32 tensor [1] (g, when given)."""
+    _dense(x, "x")
+    g = torch.empty(1, dtype=torch.float32, device=x.device) if g is None else g
+    if g.dtype != torch.float32 or g.numel() != 1 or g.device != x.device:
+        raise ValueError("g must be a float32 tensor of one value on x's device")
+    with _on_device(x):
+        _check(load().sv_mx_global_scale(_ptr(x), x.numel(), _dt(x), _ptr(g), _stream(stream)))
+    return g
+
+
+def sv_mx_quantize(x, fmt: int, gscale=None, out: MxTensor | None = None, stream=None) -> MxTensor:
+    """x to a microscaled matrix: [..., C] rows as they are, or [B, H, N, D] (four dimensions) as B * N
+    rows that hold the heads side by side. SV_NVFP4 takes the tensor scale gscale (float32 [1])."""
+    _dense(x, "x")
+    if x.dim() < 2:
+        raise ValueError("x must be [..., C] or [B, H, N, D]")
+    if x.dim() == 4:
+        B, H, N, D = x.shape
+    else:
+        B, H, D = 1, 1, x.shape[-1]
+        N = x.numel() // D if D else 0
+    out = _mx_out(out, B * N, H * D, fmt, gscale, x.device)
+    with _on_device(x):
+        _check(load().sv_mx_quantize(_ptr(x), B, H, N, D, _dt(x), out._ref, _stream(stream)))
+    return out
+
+
+def sv_mx_dequantize(xq: MxTensor, dtype=torch.bfloat16, y=None, stream=None):
+    """The values of a microscaled matrix as [rows, cols] bfloat16 or float32."""
+    y = torch.empty(xq.rows, xq.cols, dtype=dtype, device=xq.device) if y is None else y
+    if tuple(y.shape) != (xq.rows, xq.cols) or not y.is_contiguous() or y.device != xq.device:
+        raise ValueError("y must be a contiguous [rows, cols] tensor on xq's device")
+    with _on_device(y):
+        _check(load().sv_mx_dequantize(xq._ref, _ptr(y), _dt(y), _stream(stream)))
+    return y
+
+
+def sv_rmsnorm(x, w, residual=None, eps: float = 1e-6, fmt: int | None = None, gscale=None, h=None, y=None, stream=None):
+    """Root-mean-square norm over x's last dimension after the residual's addition; returns (y, h).
+
+    h = x + residual in x's dtype (x itself without a residual). y = h / rms(h) * w, in x's dtype and shape,
+    or, with fmt, quantised in the same pass to an MxTensor of one row per position (y, when given, is that
+    MxTensor; SV_NVFP4 takes gscale). h may be x or residual (in place)."""
+    _dense(x, "x")
+    C = x.shape[-1] if x.dim() else 0
+    if C == 0 or x.numel() == 0:
+        raise ValueError("x must be [..., C] with at least one row and column")
+    if w.dtype != torch.float32 or tuple(w.shape) != (C,) or not w.is_contiguous() or w.device != x.device:
+        raise ValueError("w must be a contiguous float32 [C] tensor on x's device")
+    if residual is None:
+        if h is not None and h is not x:
+            raise ValueError("without a residual h is x")
+        h = x
+    else:
+        h = torch.empty_like(x) if h is None else h
+    for t, name in ((residual, "residual"), (h, "h")):
+        if t is not None and t is not x and (t.shape != x.shape or t.dtype != x.dtype or t.device != x.device or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous tensor of x's shape, dtype and device")
+    rows = x.numel() // C
+    if fmt is None:
+        if gscale is not None:
+            raise ValueError("gscale goes with fmt=SV_NVFP4")
+        y = torch.empty_like(x) if y is None else y
+        if y.shape != x.shape or y.dtype != x.dtype or y.device != x.device or not y.is_contiguous():
+            raise ValueError("y must be a contiguous tensor of x's shape, dtype and device")
+        py, pq = y.data_ptr(), None
+    else:
+        y = _mx_out(y, rows, C, fmt, gscale, x.device)
+        py, pq = None, y._ref
+    with _on_device(x):
+        _check(load().sv_rmsnorm(_ptr(x), _ptr(residual), None if residual is None else _ptr(h), _ptr(w), rows, C, _dt(x),
+                                 eps, py, pq, _stream(stream)))
+    return y, h
+
+
+_mx_ws = {}
+
+
+def _mx_workspace(device, stream):
+    """The status workspace of the microscaled products, one per device: they use its status word only,
+    so calls on several streams share it."""
+    ws = _mx_ws.get(device.index)
+    if ws is None:
+        ws = _mx_ws[device.index] = Workspace(256, device, stream)
+    ws.check(stream)
+    return ws
+
+
+def _mx_pair(xq, wq):
+    if xq.fmt != wq.fmt or xq.cols != wq.cols or xq.device != wq.device:
+        raise ValueError("x and w must share format, number of columns and device")
+
+
+def sv_mx_projection(xq: MxTensor, wq: MxTensor, y=None, ws: Workspace | None = None, stream=None):
+    """y [xq.rows, wq.rows] bfloat16 = x W^T of two microscaled matrices. Make the first call on a device
+    (or pass ws) before capturing one into a CUDA graph."""
+    _mx_pair(xq, wq)
+    y = torch.empty(xq.rows, wq.rows, dtype=torch.bfloat16, device=xq.device) if y is None else y
+    if (y.dtype != torch.bfloat16 or y.numel() != xq.rows * wq.rows or y.shape[-1] != wq.rows or not y.is_contiguous()
+            or y.device != xq.device):
+        raise ValueError("y must be a contiguous bfloat16 tensor of x's rows and w's rows on x's device")
+    with _on_device(y):
+        ws = ws if ws is not None else _mx_workspace(xq.device, stream)
+        _check(load().sv_mx_projection(xq._ref, wq._ref, _ptr(y), ws.ptr, ws.nbytes, _stream(stream)))
+    return y
+
+
+def sv_mx_qkv_projection(xq: MxTensor, wq: MxTensor, B: int, N: int, H: int, D: int, q=None, k=None, v=None,
+                         ws: Workspace | None = None, stream=None):
+    """x of B * N rows, w of 3 * H * D rows -> (ReLU(q), ReLU(k), v), each [B, H, N, D] bfloat16. ws as for
+    sv_mx_projection."""
+    _mx_pair(xq, wq)
+    shape = (B, H, N, D)
+    q, k, v = (torch.empty(shape, dtype=torch.bfloat16, device=xq.device) if t is None else t for t in (q, k, v))
+    for t in (q, k, v):
+        if tuple(t.shape) != shape or t.dtype != torch.bfloat16 or not t.is_contiguous() or t.device != xq.device:
+            raise ValueError("q, k, v must be contiguous bfloat16 [B, H, N, D] tensors on x's device")
+    with _on_device(q):
+        ws = ws if ws is not None else _mx_workspace(xq.device, stream)
+        _check(load().sv_mx_qkv_projection(xq._ref, wq._ref, _ptr(q), _ptr(k), _ptr(v), B, N, H, D, ws.ptr, ws.nbytes,
+                                           _stream(stream)))
+    return q, k, v

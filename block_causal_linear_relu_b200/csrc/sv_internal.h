@@ -87,6 +87,25 @@ sv_status encode_bf16_4d(CUtensorMap* m, const void* base, const uint64_t dims[4
 // Records `msg` as the calling thread's sv_last_error() text and returns `status`.
 sv_status set_last_error(sv_status status, const char* msg);
 
+// ---- microscaled operands (layout in the public header) ----
+constexpr long long kMxMaxRows = 0x7fffffffLL - 255;  // rows rounded up to 128 stay below 2^31
+constexpr int mx_block(sv_mx_format f) { return f == SV_NVFP4 ? 16 : 32; }
+// columns in 128 bytes of codes, and the blocks in them
+constexpr int mx_cols_per_run(sv_mx_format f) { return f == SV_MXFP8 ? 128 : 256; }
+constexpr long long mx_row_tiles(long long rows) { return (rows + 127) / 128; }
+constexpr int mx_runs(sv_mx_format f, int cols) {
+  return cols / mx_cols_per_run(f) + (cols % mx_cols_per_run(f) != 0 ? 1 : 0);
+}
+constexpr int mx_padded_blocks(sv_mx_format f, int cols) {
+  return mx_runs(f, cols) * (mx_cols_per_run(f) / mx_block(f));
+}
+// pointers, alignment, sizes and the tensor scale of a microscaled matrix; `name` goes into the message
+sv_status check_mx(const sv_mx* m, const char* name);
+// number of SMs of the current device, which must be sm_100 (looked up once per device)
+sv_status mx_device(int* sms);
+// a 2-D byte map [rows, bytes] of codes with boxes of box_rows x 128 bytes, 128-byte swizzle
+sv_status encode_bytes_2d(CUtensorMap* m, const void* base, uint64_t bytes, uint64_t rows, uint32_t box_rows);
+
 size_t state_bf16_smem_bytes();
 size_t out_bf16_smem_bytes();
 size_t state_f32_smem_bytes();

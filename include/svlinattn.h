@@ -259,6 +259,84 @@ sv_status sv_qkv_projection(const void* x, const void* w_qkv, void* q, void* k, 
 sv_status sv_out_projection(const void* o, const void* w_o, void* y, int B, int N, int H, int D, int C_out, void* ws,
                             size_t ws_bytes, sv_stream_t stream);
 
+/* Microscaled operands: 8- and 4-bit floating point elements that share a scale per block of
+ * consecutive columns (SANA-Video abstract: deployment in NVFP4; OCP Microscaling formats 1.0).
+ *     value = element * block scale [* tensor scale]
+ *   SV_MXFP8  e4m3 elements, blocks of 32, e8m0 scales (a power of two each)
+ *   SV_MXFP4  e2m1 elements, blocks of 32, e8m0 scales
+ *   SV_NVFP4  e2m1 elements, blocks of 16, e4m3 scales, and one fp32 scale g > 0 for the tensor
+ * Quantisation of a block whose largest magnitude is a:
+ *   SV_MXFP8 / SV_MXFP4: scale s = the smallest power of two >= 2^-127 with a <= s * 448 (or 6), so
+ *   that nothing saturates;  SV_NVFP4: s = e4m3(a / (6 g)).
+ *   element = x / s (or x / (s g)). Each quotient is rounded once, to nearest, ties to even, and stops
+ *   at the type's largest value; a block with s = 0 has zero elements.
+ *   If a (or g) is infinite or NaN, the block's scale is NaN and its elements are zero: every value of
+ *   the block then reads as NaN, and so does every product that uses it.
+ * Layout of a matrix of `rows` rows and `cols` columns (a multiple of 32):
+ *   codes  [rows][cols] bytes (SV_MXFP8) or [rows][cols / 2] bytes, two elements to a byte, the even
+ *          column in the low half;
+ *   scales [ceil(rows / 128)][P / 4][32][4][4] bytes: the scale of row r and block j sits at
+ *          [r / 128][j / 4][r % 32][(r / 32) % 4][j % 4]. P is the number of blocks, rounded up so that
+ *          P blocks fill whole 128-byte runs of codes (a multiple of 4, 8 or 16 for SV_MXFP8, SV_MXFP4,
+ *          SV_NVFP4). Places without a block hold zero. */
+typedef enum { SV_MXFP8 = 0, SV_MXFP4 = 1, SV_NVFP4 = 2 } sv_mx_format;
+
+typedef struct {
+  void* codes;         /* DEVICE, 16-byte aligned, sv_mx_code_bytes(...) bytes */
+  void* scales;        /* DEVICE, 16-byte aligned, sv_mx_scale_bytes(...) bytes */
+  const float* gscale; /* DEVICE fp32 g (SV_NVFP4, 4-byte aligned); NULL for the other formats */
+  long long rows;
+  int cols;
+  sv_mx_format fmt;
+} sv_mx;
+
+/* Bytes of the codes and of the scales of a rows x cols matrix; 0 for arguments out of range (rows < 1
+ * or > 2^31 - 256, cols < 32 or not a multiple of 32, or an unknown format; see sv_last_error). */
+size_t sv_mx_code_bytes(sv_mx_format fmt, long long rows, int cols);
+size_t sv_mx_scale_bytes(sv_mx_format fmt, long long rows, int cols);
+
+/* The tensor scale of SV_NVFP4 that makes the largest magnitude of x representable:
+ * *g = max |x_i| / (6 * 448), rounded to fp32 (NaN if x holds a NaN). x: n >= 1 elements of dt, 16-byte
+ * aligned; g: DEVICE fp32, 4-byte aligned. */
+sv_status sv_mx_global_scale(const void* x, long long n, sv_dtype dt, float* g, sv_stream_t stream);
+
+/* Quantises x [B, H, N, D] (contiguous, type dt, 16-byte aligned) to the matrix out of B * N rows and
+ * H * D columns: row b * N + n holds the heads of token n side by side (the order in which
+ * sv_out_projection reads them). H = 1 quantises plain rows. D a multiple of 8, H * D of 32.
+ * out (HOST pointer, read during the call) must have rows = B * N and cols = H * D. */
+sv_status sv_mx_quantize(const void* x, int B, int H, int N, int D, sv_dtype dt, const sv_mx* out, sv_stream_t stream);
+
+/* The values of a microscaled matrix: y [rows, cols] of type dt (16-byte aligned), computed in fp32
+ * (element * scale exactly, then * g) and rounded to dt. */
+sv_status sv_mx_dequantize(const sv_mx* in, void* y, sv_dtype dt, sv_stream_t stream);
+
+/* Root-mean-square norm with the residual's addition, the step before a projection:
+ *     h = x + residual (rounded to dt),   y = h / sqrt(mean_c(h_c^2) + eps) * w
+ * x, residual, h: DEVICE [rows, C] of dt; residual NULL: h = x, and then h may be NULL (not written).
+ * h may equal x or residual (in place). w: DEVICE fp32 [C]. The output goes to one of
+ *   y  (DEVICE [rows, C] of dt; may equal x if h does not), or
+ *   yq (HOST pointer to a microscaled matrix of rows x C): y is quantised before any rounding to dt,
+ *      so no unquantised copy is written;
+ * the other is NULL. The squares are summed in fp64, so y does not depend on how the sum is split.
+ * C at most 32768, a multiple of 8, and of 32 with yq; pointers 16-byte aligned. */
+sv_status sv_rmsnorm(const void* x, const void* residual, void* h, const float* w, long long rows, int C, sv_dtype dt,
+                     float eps, void* y, const sv_mx* yq, sv_stream_t stream);
+
+/* Product of two microscaled matrices of one format and one number of columns, the linear map
+ *     y = x W^T   (y[r][f] = sum_c x[r][c] W[f][c]),
+ * on the block-scaled tensor-core path: fp32 accumulation, one bf16 rounding. x: tokens (rows), w:
+ * weight (one row per output feature, a multiple of 8). y: DEVICE bf16 [x.rows, w.rows], 16-byte
+ * aligned. With x quantised from the attention output this is the output projection. x and w are HOST
+ * pointers, read during the call. ws: a workspace of at least 256 bytes (sv_workspace_init), whose
+ * status word reports a device-side timeout (sv_device_status). */
+sv_status sv_mx_projection(const sv_mx* x, const sv_mx* w, void* y, void* ws, size_t ws_bytes, sv_stream_t stream);
+
+/* sv_qkv_projection on microscaled operands: x has B * N rows (row b * N + n is token n of batch b), w
+ * has 3 * H * D rows (Q features, then K, then V); q = ReLU(.), k = ReLU(.), v linear, each DEVICE bf16
+ * [B, H, N, D], 16-byte aligned. D = 64 or 128. ws as for sv_mx_projection. */
+sv_status sv_mx_qkv_projection(const sv_mx* x, const sv_mx* w, void* q, void* k, void* v, int B, int N, int H, int D,
+                               void* ws, size_t ws_bytes, sv_stream_t stream);
+
 /* Optional timing hook for benchmarks. With events != NULL (n == 4 cudaEvent_t handles owned by
  * the caller), the calling thread's following forward calls (sv_linattn_fwd, sv_block_causal_attn,
  * sv_cache_step) record events[0] before the state-reduction kernel, events[1] after it,
