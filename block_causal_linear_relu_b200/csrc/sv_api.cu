@@ -176,6 +176,20 @@ sv_status encode_bytes_2d(CUtensorMap* m, const void* base, uint64_t bytes, uint
   if (r != CUDA_SUCCESS) return fail(SV_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", static_cast<int>(r));
   return SV_OK;
 }
+
+sv_status encode_scale_tiles(CUtensorMap* m, const void* base, uint64_t tiles, uint32_t box_tiles) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return fail(SV_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  cuuint64_t d[2] = {128, tiles};
+  cuuint64_t st[1] = {512};
+  cuuint32_t bx[2] = {128, box_tiles};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), d, st, bx, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(SV_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", static_cast<int>(r));
+  return SV_OK;
+}
 }  // namespace sv
 
 namespace {

@@ -105,6 +105,8 @@ sv_status check_mx(const sv_mx* m, const char* name);
 sv_status mx_device(int* sms);
 // a 2-D byte map [rows, bytes] of codes with boxes of box_rows x 128 bytes, 128-byte swizzle
 sv_status encode_bytes_2d(CUtensorMap* m, const void* base, uint64_t bytes, uint64_t rows, uint32_t box_rows);
+// scale tiles as a 2-D map [tiles, 512 bytes] with boxes of box_tiles tiles, no swizzle
+sv_status encode_scale_tiles(CUtensorMap* m, const void* base, uint64_t tiles, uint32_t box_tiles);
 
 size_t state_bf16_smem_bytes();
 size_t out_bf16_smem_bytes();

@@ -6,13 +6,17 @@
 // formats use one pipeline, because a 128-byte run of codes is four K steps of 32 bytes in each:
 // 128 columns of e4m3 (K = 32 a step) or 256 columns of e2m1 (K = 64 a step).
 //
-// A persistent kernel, one CTA per SM, 128 x 128 output tiles. A stage holds a run of A and of B (128
-// rows x 128 bytes each, 128-byte swizzle) and their scale tiles (512 bytes per four blocks of K, stored
-// in the order in which TMEM wants them, so a plain bulk copy fetches them). Warp 0 issues the copies;
-// warp 1 copies a stage's scales to TMEM and issues its four MMAs into one of two fp32 accumulators;
-// warps 2-5 drain the other: the tensor scales, bf16, ReLU, a swizzled buffer, and row-coalesced
-// 16-byte stores. A tile's rows are consecutive rows of X, whatever batch they belong to, because the
-// scale tiles run over all rows; the stores find each row's batch and token.
+// A persistent kernel of CTA pairs (cta_group::2): an output tile has 256 rows and NT columns; each CTA of
+// a pair holds 128 rows of A and NT / 2 of B in its shared memory, and the pair's MMA reads both, so a
+// byte of shared memory feeds twice the products that it would in one CTA (with 128 x 128 tiles of one
+// CTA the 4-bit kinds need the whole 128 bytes per cycle of shared memory). Few rows take 128 x 64 tiles
+// of single CTAs: then the weight's stream bounds the call, and more CTAs stream faster.
+// A stage holds a 128-byte run of A and B (128-byte swizzle) and their scale tiles (512 bytes per four
+// blocks of K, stored in the order in which TMEM wants them). Warp 0 of each CTA issues the copies; warp 1
+// of the even CTA copies a stage's scales to TMEM and issues its four MMAs into one of two fp32
+// accumulators; warps 2-5 of each CTA drain the other: the tensor scales, bf16, ReLU, a swizzled buffer,
+// and row-coalesced 16-byte stores. A tile's rows are consecutive rows of X, whatever batch they belong
+// to, because the scale tiles run over all rows; the stores find each row's batch and token.
 // Rows past the last one and runs past K are zero-filled by the tensor maps; their scales are zero
 // bytes, which both scale types read as finite numbers.
 #include <cuda.h>
@@ -28,59 +32,69 @@
 namespace sv {
 namespace {
 
-constexpr int kM = 128, kN = 128;
-constexpr int kRunBytes = 128 * 128;  // one run of one operand: 128 rows x 128 bytes
-constexpr int kThreads = 192;         // warp 0 copies, warp 1 MMAs, warps 2-5 epilogue
-constexpr int kStaging = 32 * 128;    // per epilogue warp: 32 rows x 64 bf16
+constexpr int kRows = 128;          // rows of A per CTA
+constexpr int kThreads = 192;       // warp 0 copies, warp 1 MMAs, warps 2-5 epilogue
+constexpr int kStaging = 32 * 128;  // per epilogue warp: 32 rows x 64 bf16
 
-template <int FMT>
+template <int FMT, int CTAS, int NT>
 struct Cfg {
   static constexpr int kTiles = FMT == SV_NVFP4 ? 4 : FMT == SV_MXFP4 ? 2 : 1;  // scale tiles per run and 128 rows
   static constexpr int kScaleBytes = kTiles * 512;
-  static constexpr int kStageBytes = 2 * kRunBytes + 2 * kScaleBytes;
-  static constexpr int kStages = 5;
-  static constexpr int kStagingOff = kStages * kStageBytes;
+  static constexpr int kBBlocks = NT > 128 ? 2 : 1;  // 128-row scale blocks that a column tile touches
+  static constexpr int kABytes = kRows * 128;
+  static constexpr int kBBytes = NT / CTAS * 128;
+  static constexpr int kStageBytes = kABytes + kBBytes + (1 + kBBlocks) * kScaleBytes;
+  static constexpr int kStride = (kStageBytes + 1023) / 1024 * 1024;  // the swizzle's alignment
+  static constexpr int kFit = (226 * 1024 - 4 * kStaging - 1536) / kStride;
+  static constexpr int kStages = kFit < 8 ? kFit : 8;
+  static constexpr int kStagingOff = kStages * kStride;
   static constexpr int kBarOff = kStagingOff + 4 * kStaging;
   static constexpr int kSmem = kBarOff + 256 + 1024;  // barriers, TMEM slot, alignment slack
-  static_assert(kSmem <= 227 * 1024, "shared memory of the microscaled product");
-  static_assert(kStageBytes % 1024 == 0, "stages keep the swizzle's 1024-byte alignment");
+  static_assert(kSmem <= 227 * 1024 && kStages >= 4, "shared memory of the microscaled product");
+  // TMEM columns: two accumulators of NT, then two buffers of scales (A: 4 per tile, B: 4 per tile and block)
+  static constexpr uint32_t kScaleCols = 4 * kTiles * (1 + kBBlocks);
+  static constexpr uint32_t kScaleCol = 2 * NT;
+  static_assert(kScaleCol + 2 * kScaleCols <= 512, "TMEM columns");
+  static constexpr MxKind kKind = FMT == SV_MXFP8 ? kMx8 : FMT == SV_MXFP4 ? kMx4 : kNv4;
 };
 
-// TMEM columns: two accumulators, then the scales of two stages (A: 4 per tile, B: 4 per tile)
-constexpr uint32_t kScaleCol = 2 * kN;
-constexpr uint32_t kScaleColsPerStage = 32;
-
 struct Geo {
-  int rows;        // rows of X
-  int nout;        // output features
-  int runs;        // 128-byte runs of K
-  int nt;          // column tiles
-  int tiles;       // all tiles, column tile fastest
-  int N, H, D;     // Q/K/V only: tokens per batch, heads, head features
+  int rows;     // rows of X
+  int nout;     // output features
+  int runs;     // 128-byte runs of K
+  int nt;       // column tiles
+  int tiles;    // all tiles, column tile fastest
+  int N, H, D;  // Q/K/V only: tokens per batch, heads, head features
+};
+
+struct Maps {
+  CUtensorMap a, b;    // codes: [rows, bytes], boxes of 128 rows (A) or NT / CTAS rows (B) x 128 bytes
+  CUtensorMap sa, sb;  // scale tiles: [tiles, 512 bytes], boxes of a run's tiles
 };
 
 struct Ops {
-  const uint8_t *sa, *sb;    // scale tiles of X and W
-  const float *ga, *gb;      // tensor scales, or NULL
+  const float *ga, *gb;         // tensor scales, or NULL
   __nv_bfloat16 *o0, *o1, *o2;  // y, or q, k, v
 };
 
 __device__ __forceinline__ bool warp_all(bool ok) { return __all_sync(0xffffffffu, ok); }
 
-template <int FMT, bool kQKV>
+template <int FMT, int CTAS, int NT, bool kQKV>
 __global__ void __launch_bounds__(kThreads, 1)
-    mxproj_kernel(const __grid_constant__ CUtensorMap a_map, const __grid_constant__ CUtensorMap b_map, const Ops op,
-                  const Geo g, uint32_t* status) {
-  using C = Cfg<FMT>;
+    mxproj_kernel(const __grid_constant__ Maps maps, const Ops op, const Geo g, uint32_t* status) {
+  using C = Cfg<FMT, CTAS, NT>;
   extern __shared__ uint8_t smem_raw[];
+  // the dynamic shared memory starts at the same offset in both CTAs of a pair, and so does `smem`
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);  // [kStages] a run of both operands landed
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kBarOff);  // [kStages] a run landed (the even CTA's counts both)
   uint64_t* empty = full + C::kStages;                              // [kStages] the run's MMAs retired
   uint64_t* accf = empty + C::kStages;                              // [2] accumulator holds a finished tile
-  uint64_t* acce = accf + 2;                                        // [2] accumulator drained
+  uint64_t* acce = accf + 2;                                        // [2] accumulator drained (the even CTA's)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acce + 2);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  const int rank = CTAS == 2 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int first = static_cast<int>(blockIdx.x) / CTAS, step = static_cast<int>(gridDim.x) / CTAS;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&full[i], 1);
@@ -88,18 +102,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&accf[a], 1);
-      mbar_init(&acce[a], 4);
+      mbar_init(&acce[a], 4 * CTAS);
     }
     fence_mbar_init();
-    prefetch_tmap(&a_map);
-    prefetch_tmap(&b_map);
+    prefetch_tmap(&maps.a);
+    prefetch_tmap(&maps.b);
+    prefetch_tmap(&maps.sa);
+    prefetch_tmap(&maps.sb);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, 512);
-    tmem_relinquish();
+    if (CTAS == 1) {
+      tmem_alloc(tmem_slot, 512);
+      tmem_relinquish();
+    } else {
+      tmem_alloc_pair(tmem_slot, 512);
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if (CTAS == 2) {  // the other CTA's barriers are ready
+    cluster_arrive_release();
+    cluster_wait_acquire();
+  }
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   griddep_wait();  // the previous kernel may still write the operands or read the outputs
@@ -111,80 +135,115 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t pol_b = policy_evict_last();  // W is read by every row tile
       int it = 0;
       bool ok = true;
-      for (int tile = blockIdx.x; tile < g.tiles && ok; tile += gridDim.x) {
-        const int m = tile / g.nt, n = tile - m * g.nt;
+      for (int tile = first; tile < g.tiles && ok; tile += step) {
+        const int m = tile / g.nt, n0 = (tile - m * g.nt) * NT;
+        const int ma = m * CTAS + rank;  // this CTA's 128 rows
         for (int kc = 0; kc < g.runs; ++kc, ++it) {
           const int s = it % C::kStages;
           if (!mbar_wait(&empty[s], ((it / C::kStages) & 1) ^ 1, status, 0x6100u | s)) {
             ok = false;
             break;
           }
-          uint8_t* st = smem + s * C::kStageBytes;
-          mbar_expect_tx(&full[s], C::kStageBytes);
-          tma_load_2d(st, &a_map, &full[s], kc * 128, m * kM, pol_a);
-          tma_load_2d(st + kRunBytes, &b_map, &full[s], kc * 128, n * kN, pol_b);
-          uint8_t* sc = st + 2 * kRunBytes;
-          bulk_load(sc, op.sa + (static_cast<size_t>(m) * g.runs + kc) * C::kScaleBytes, C::kScaleBytes, &full[s]);
-          bulk_load(sc + C::kScaleBytes, op.sb + (static_cast<size_t>(n) * g.runs + kc) * C::kScaleBytes, C::kScaleBytes,
-                    &full[s]);
+          uint8_t* sa = smem + s * C::kStride;
+          uint8_t* sb = sa + C::kABytes;
+          uint8_t* sc = sb + C::kBBytes;
+          const int ta = (ma * g.runs + kc) * C::kTiles;
+          if (CTAS == 1) {
+            mbar_expect_tx(&full[s], C::kStageBytes);
+            tma_load_2d(sa, &maps.a, &full[s], kc * 128, ma * kRows, pol_a);
+            tma_load_2d(sb, &maps.b, &full[s], kc * 128, n0, pol_b);
+            tma_load_2d(sc, &maps.sa, &full[s], 0, ta, pol_a);
+#pragma unroll
+            for (int j = 0; j < C::kBBlocks; ++j)
+              tma_load_2d(sc + (1 + j) * C::kScaleBytes, &maps.sb, &full[s], 0,
+                          ((n0 / 128 + j) * g.runs + kc) * C::kTiles, pol_b);
+          } else {
+            const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
+            if (rank == 0) mbar_expect_tx(&full[s], 2 * C::kStageBytes);
+            tma_load_2d_pair(sa, &maps.a, bar, kc * 128, ma * kRows, pol_a);
+            tma_load_2d_pair(sb, &maps.b, bar, kc * 128, n0 + rank * (NT / 2), pol_b);
+            tma_load_2d_pair(sc, &maps.sa, bar, 0, ta, pol_a);
+#pragma unroll
+            for (int j = 0; j < C::kBBlocks; ++j)  // both CTAs need the scales of all NT columns
+              tma_load_2d_pair(sc + (1 + j) * C::kScaleBytes, &maps.sb, bar, 0,
+                               ((n0 / 128 + j) * g.runs + kc) * C::kTiles, pol_b);
+          }
         }
       }
+      // the last runs' MMAs report to this CTA's barriers: stay until they have
+      for (int i = it < C::kStages ? 0 : it - C::kStages; i < it && ok; ++i)
+        ok = mbar_wait(&empty[i % C::kStages], (i / C::kStages) & 1, status, 0x6180u | (i % C::kStages));
     }
   } else if (warp == 1) {
-    if (lane == 0) {  // scales and MMAs
+    if (lane == 0 && rank == 0) {  // scales and MMAs
       int it = 0, tl = 0;
       bool ok = true;
-      for (int tile = blockIdx.x; tile < g.tiles && ok; tile += gridDim.x, ++tl) {
+      for (int tile = first; tile < g.tiles && ok; tile += step, ++tl) {
         const int a = tl & 1;
         if (!mbar_wait(&acce[a], ((tl >> 1) & 1) ^ 1, status, 0x6300u | a)) break;
         tc_fence_after();
-        const uint32_t d = tmem + static_cast<uint32_t>(a * kN);
+        const uint32_t d = tmem + static_cast<uint32_t>(a * NT);
+        const int n0 = (tile % g.nt) * NT;
+        const uint32_t shift = static_cast<uint32_t>(n0 % 128) / 32;  // columns of B's first scale block before the tile
         for (int kc = 0; kc < g.runs; ++kc, ++it) {
           const int s = it % C::kStages;
           if (!mbar_wait(&full[s], (it / C::kStages) & 1, status, 0x6310u | s)) {
             ok = false;
             break;
           }
+          // the MMAs that read this buffer of scales two runs ago have retired
+          if (it >= 2 && !mbar_wait(&empty[(it - 2) % C::kStages], ((it - 2) / C::kStages) & 1, status, 0x6320u | s)) {
+            ok = false;
+            break;
+          }
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + s * C::kStageBytes);
-          const uint32_t sb = sa + kRunBytes;
-          const uint32_t sc = sb + kRunBytes;
-          const uint32_t ta = tmem + kScaleCol + static_cast<uint32_t>(it & 1) * kScaleColsPerStage;
+          const uint32_t sa = smem_u32(smem + s * C::kStride);
+          const uint32_t sb = sa + C::kABytes;
+          const uint32_t sc = sb + C::kBBytes;
+          const uint32_t ta = tmem + C::kScaleCol + static_cast<uint32_t>(it & 1) * C::kScaleCols;
           const uint32_t tb = ta + 4 * C::kTiles;
 #pragma unroll
           for (int t = 0; t < C::kTiles; ++t) {
-            tmem_copy_scales(ta + 4 * t, sc + 512 * t);
-            tmem_copy_scales(tb + 4 * t, sc + C::kScaleBytes + 512 * t);
+            tmem_copy_scales<CTAS>(ta + 4 * t, sc + 512 * t);
+#pragma unroll
+            for (int j = 0; j < C::kBBlocks; ++j)
+              tmem_copy_scales<CTAS>(tb + 4 * (t * C::kBBlocks + j), sc + (1 + j) * C::kScaleBytes + 512 * t);
           }
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t da = sdesc_sw128(sa + kk * 32, 16, 1024), db = sdesc_sw128(sb + kk * 32, 16, 1024);
-            const uint32_t acc = (kc | kk) != 0 ? 1u : 0u;
-            if (FMT == SV_MXFP8)
-              mma_mxf8(d, da, db, idesc_mx(kM, kN, 0, true, kk), ta, tb, acc);
-            else if (FMT == SV_MXFP4)
-              mma_mxf4(d, da, db, idesc_mx(kM, kN, 1, true, (kk & 1) * 2), ta + 4 * (kk >> 1), tb + 4 * (kk >> 1), acc);
-            else
-              mma_nvf4(d, da, db, idesc_mx(kM, kN, 1, false, 0), ta + 4 * kk, tb + 4 * kk, acc);
+            // step kk: scale tile t, byte id of its 32-bit cells
+            const int t = FMT == SV_NVFP4 ? kk : FMT == SV_MXFP4 ? kk >> 1 : 0;
+            const uint32_t id = FMT == SV_NVFP4 ? 0 : FMT == SV_MXFP4 ? (kk & 1) * 2 : kk;
+            mma_mx<CTAS, C::kKind>(d, sdesc_sw128(sa + kk * 32, 16, 1024), sdesc_sw128(sb + kk * 32, 16, 1024),
+                                   idesc_mx(kRows * CTAS, NT, FMT == SV_MXFP8 ? 0 : 1, FMT != SV_NVFP4, id), ta + 4 * t,
+                                   tb + 4 * C::kBBlocks * t + shift, (kc | kk) != 0 ? 1u : 0u);
           }
-          mma_commit(&empty[s]);
+          if (CTAS == 1)
+            mma_commit(&empty[s]);
+          else
+            mma_commit_pair(&empty[s]);
         }
-        if (ok) mma_commit(&accf[a]);
+        if (ok) {
+          if (CTAS == 1)
+            mma_commit(&accf[a]);
+          else
+            mma_commit_pair(&accf[a]);
+        }
       }
     }
-  } else {  // epilogue: warp w drains TMEM lanes 32 * (w % 4) .. + 31 (rows of the tile)
+  } else {  // epilogue: warp w drains TMEM lanes 32 * (w % 4) .. + 31 (rows of this CTA's half)
     const int q = warp & 3;
     uint8_t* stg = smem + C::kStagingOff + (warp - 2) * kStaging;
     const float alpha = FMT == SV_NVFP4 ? *op.ga * *op.gb : 1.f;
     const int sub = lane >> 3, piece = lane & 7;  // store step i: row 4 i + sub, 16-byte piece of its 128 bytes
     int tl = 0;
-    for (int tile = blockIdx.x; tile < g.tiles; tile += gridDim.x, ++tl) {
+    for (int tile = first; tile < g.tiles; tile += step, ++tl) {
       const int a = tl & 1;
       if (!warp_all(mbar_wait(&accf[a], (tl >> 1) & 1, status, 0x6400u | a))) break;
       tc_fence_after();
-      const int m = tile / g.nt, n = tile - m * g.nt;
-      const int row0 = m * kM + q * 32;
-      const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(a * kN);
+      const int m = tile / g.nt, n0 = (tile - m * g.nt) * NT;
+      const int row0 = (m * CTAS + rank) * kRows + q * 32;
+      const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(a * NT);
       size_t at[8];  // element offsets of the rows that this lane stores
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -197,17 +256,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
 #pragma unroll 1
-      for (int c = 0; c < kN / 64; ++c) {
+      for (int c = 0; c < NT / 64; ++c) {
         uint32_t rr[2][32];
         tmem_ld_x32(ta + c * 64, rr[0]);
         tmem_ld_x32(ta + c * 64 + 32, rr[1]);
         tmem_wait_ld();
-        if (c == kN / 64 - 1) {  // the tile's last TMEM read: the accumulator is free
+        if (c == NT / 64 - 1) {  // the tile's last TMEM read: the accumulator is free
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&acce[a]);
+          if (lane == 0) {
+            if (CTAS == 1)
+              mbar_arrive(&acce[a]);
+            else
+              mbar_arrive_cluster(mapa_shared(smem_u32(&acce[a]), 0));
+          }
         }
-        const int nc = n * kN + c * 64;  // first output feature of the chunk
+        const int nc = n0 + c * 64;  // first output feature of the chunk
         if (nc >= g.nout) continue;
         __nv_bfloat16* out = op.o0;
         bool relu = false;
@@ -243,9 +307,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (CTAS == 2) {  // neither CTA leaves while the other may still signal its barriers or read its operands
+    cluster_arrive_release();
+    cluster_wait_acquire();
+  }
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    if (CTAS == 1)
+      tmem_dealloc(tmem, 512);
+    else
+      tmem_dealloc_pair(tmem, 512);
   }
 }
 
@@ -262,7 +333,7 @@ sv_status pfail(sv_status st, const char* fmt, long long a = 0, long long b = 0)
   } while (0)
 
 // The kernel's shared-memory attribute, set once per device (and per kernel), thread-safe.
-template <int FMT, bool kQKV>
+template <int FMT, int CTAS, int NT, bool kQKV>
 cudaError_t ensure_attr() {
   constexpr int kMaxDev = 64;
   static std::mutex mu;
@@ -273,31 +344,63 @@ cudaError_t ensure_attr() {
   if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lock(mu);
   if (!done[dev]) {
-    e = cudaFuncSetAttribute(mxproj_kernel<FMT, kQKV>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<FMT>::kSmem);
+    e = cudaFuncSetAttribute(mxproj_kernel<FMT, CTAS, NT, kQKV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Cfg<FMT, CTAS, NT>::kSmem);
     if (e != cudaSuccess) return e;
     done[dev] = true;
   }
   return cudaSuccess;
 }
 
-template <int FMT, bool kQKV>
-sv_status run(const CUtensorMap& am, const CUtensorMap& bm, const Ops& op, const Geo& g, void* ws, int sms, cudaStream_t st) {
-  cudaError_t e = ensure_attr<FMT, kQKV>();
+template <int FMT, int CTAS, int NT, bool kQKV>
+sv_status run(const sv_mx& x, const sv_mx& w, const Ops& op, Geo g, void* ws, int sms, cudaStream_t st) {
+  using C = Cfg<FMT, CTAS, NT>;
+  g.nt = (g.nout + NT - 1) / NT;
+  const long long tiles = (x.rows + kRows * CTAS - 1) / (kRows * CTAS) * g.nt;
+  // scale tiles and output tiles are counted in 32 bits
+  const long long sa = mx_row_tiles(x.rows) * g.runs * C::kTiles, sb = mx_row_tiles(w.rows) * g.runs * C::kTiles;
+  if (tiles > 0x3fffffffLL || sa > 0x3fffffffLL || sb > 0x3fffffffLL)
+    return pfail(SV_ERR_UNSUPPORTED, "too many output tiles or scale tiles");
+  g.tiles = static_cast<int>(tiles);
+  const uint64_t bytes = static_cast<uint64_t>(FMT == SV_MXFP8 ? x.cols : x.cols / 2);
+  Maps maps;
+  MXP_TRY(encode_bytes_2d(&maps.a, x.codes, bytes, static_cast<uint64_t>(x.rows), kRows));
+  MXP_TRY(encode_bytes_2d(&maps.b, w.codes, bytes, static_cast<uint64_t>(w.rows), NT / CTAS));
+  MXP_TRY(encode_scale_tiles(&maps.sa, x.scales, static_cast<uint64_t>(sa), C::kTiles));
+  MXP_TRY(encode_scale_tiles(&maps.sb, w.scales, static_cast<uint64_t>(sb), C::kTiles));
+  cudaError_t e = ensure_attr<FMT, CTAS, NT, kQKV>();
   if (e == cudaSuccess) {
+    const int groups = sms / CTAS;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(g.tiles < sms ? g.tiles : sms));
+    cfg.gridDim = dim3(static_cast<unsigned>((g.tiles < groups ? g.tiles : groups) * CTAS));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Cfg<FMT>::kSmem;
+    cfg.dynamicSmemBytes = C::kSmem;
     cfg.stream = st;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = CTAS;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, mxproj_kernel<FMT, kQKV>, am, bm, op, g, static_cast<uint32_t*>(ws));
+    cfg.numAttrs = CTAS == 2 ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, mxproj_kernel<FMT, CTAS, NT, kQKV>, maps, op, g, static_cast<uint32_t*>(ws));
   }
   if (e != cudaSuccess) return pfail(SV_ERR_CUDA, "microscaled product launch failed (%lld)", static_cast<long long>(e));
   return SV_OK;
+}
+
+template <int FMT, bool kQKV>
+sv_status choose(const sv_mx& x, const sv_mx& w, const Ops& op, const Geo& g, void* ws, int sms, cudaStream_t st) {
+  if (x.rows <= 128) return run<FMT, 1, 64, kQKV>(x, w, op, g, ws, sms, st);
+  // the column tile whose last wave wastes less: waves times columns
+  const auto cost = [&](int nt) {
+    const long long tiles = (x.rows + 255) / 256 * ((w.rows + nt - 1) / nt);
+    return (tiles + sms / 2 - 1) / (sms / 2) * nt;
+  };
+  if (cost(128) < cost(192)) return run<FMT, 2, 128, kQKV>(x, w, op, g, ws, sms, st);
+  return run<FMT, 2, 192, kQKV>(x, w, op, g, ws, sms, st);
 }
 
 template <bool kQKV>
@@ -309,24 +412,14 @@ sv_status product(const sv_mx& x, const sv_mx& w, const Ops& outs, Geo g, void* 
   g.rows = static_cast<int>(x.rows);
   g.nout = static_cast<int>(w.rows);
   g.runs = mx_runs(x.fmt, x.cols);
-  g.nt = (g.nout + kN - 1) / kN;
-  const long long tiles = mx_row_tiles(x.rows) * g.nt;
-  if (tiles > 0x3fffffffLL) return pfail(SV_ERR_UNSUPPORTED, "too many output tiles");
-  g.tiles = static_cast<int>(tiles);
   int sms = 0;
   MXP_TRY(mx_device(&sms));
   Ops op = outs;
-  op.sa = static_cast<const uint8_t*>(x.scales);
-  op.sb = static_cast<const uint8_t*>(w.scales);
   op.ga = x.gscale;
   op.gb = w.gscale;
-  const uint64_t bytes = static_cast<uint64_t>(x.fmt == SV_MXFP8 ? x.cols : x.cols / 2);
-  CUtensorMap am, bm;
-  MXP_TRY(encode_bytes_2d(&am, x.codes, bytes, static_cast<uint64_t>(x.rows), kM));
-  MXP_TRY(encode_bytes_2d(&bm, w.codes, bytes, static_cast<uint64_t>(w.rows), kN));
-  if (x.fmt == SV_MXFP8) return run<SV_MXFP8, kQKV>(am, bm, op, g, ws, sms, st);
-  if (x.fmt == SV_MXFP4) return run<SV_MXFP4, kQKV>(am, bm, op, g, ws, sms, st);
-  return run<SV_NVFP4, kQKV>(am, bm, op, g, ws, sms, st);
+  if (x.fmt == SV_MXFP8) return choose<SV_MXFP8, kQKV>(x, w, op, g, ws, sms, st);
+  if (x.fmt == SV_MXFP4) return choose<SV_MXFP4, kQKV>(x, w, op, g, ws, sms, st);
+  return choose<SV_NVFP4, kQKV>(x, w, op, g, ws, sms, st);
 }
 
 bool out16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0u; }

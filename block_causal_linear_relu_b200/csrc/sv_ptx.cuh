@@ -185,45 +185,75 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64
       : "memory");
 }
 // The same on block-scaled operands: one scale per 32 (e4m3) or 16 / 32 (e2m1) elements of K, read from
-// TMEM. kind::mxf8f6f4: K = 32, scales e8m0; kind::mxf4: K = 64, scales e8m0, two per row;
-// kind::mxf4nvf4 with scale_vec::4X: K = 64, scales e4m3, four per row.
-__device__ __forceinline__ void mma_mxf8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                         uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(
-          d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
-      : "memory");
+// TMEM. kMx8: kind::mxf8f6f4, K = 32, scales e8m0; kMx4: kind::mxf4, K = 64, scales e8m0, two per row;
+// kNv4: kind::mxf4nvf4, K = 64, scales e4m3, four per row. CTAS = 2: the pair's MMA over both CTAs' shared
+// memory and TMEM (the operands at the same offsets in both), issued by the even CTA of the pair.
+enum MxKind { kMx8, kMx4, kNv4 };
+#define SV_MMA_MX(group, kind)                                                                                     \
+  asm volatile(                                                                                                    \
+      "{\n\t.reg .pred p;\n\t"                                                                                     \
+      "setp.ne.b32 p, %6, 0;\n\t"                                                                                  \
+      "tcgen05.mma.cta_group::" group "." kind " [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d_tmem), "l"(adesc), \
+      "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)                                        \
+      : "memory")
+template <int CTAS, MxKind KIND>
+__device__ __forceinline__ void mma_mx(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa_tmem,
+                                       uint32_t sfb_tmem, uint32_t accumulate) {
+  if (CTAS == 1) {
+    if (KIND == kMx8) SV_MMA_MX("1", "kind::mxf8f6f4.block_scale.scale_vec::1X");
+    if (KIND == kMx4) SV_MMA_MX("1", "kind::mxf4.block_scale.scale_vec::2X");
+    if (KIND == kNv4) SV_MMA_MX("1", "kind::mxf4nvf4.block_scale.scale_vec::4X");
+  } else {
+    if (KIND == kMx8) SV_MMA_MX("2", "kind::mxf8f6f4.block_scale.scale_vec::1X");
+    if (KIND == kMx4) SV_MMA_MX("2", "kind::mxf4.block_scale.scale_vec::2X");
+    if (KIND == kNv4) SV_MMA_MX("2", "kind::mxf4nvf4.block_scale.scale_vec::4X");
+  }
 }
-__device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                         uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(
-          d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
-      : "memory");
-}
-__device__ __forceinline__ void mma_nvf4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                         uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(
-          d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
-      : "memory");
-}
+#undef SV_MMA_MX
 // 512 bytes of scales (32 rows of 16 bytes) from shared memory to four TMEM columns, repeated in the
-// four 32-lane quarters; ordered before the MMAs that this thread issues afterwards
+// four 32-lane quarters; ordered before the MMAs that this thread issues afterwards. CTAS = 2: each CTA of
+// the pair copies from its own shared memory to its own TMEM, at the same offsets.
+template <int CTAS>
 __device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint32_t saddr) {
   const uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) |  // no swizzle
                      static_cast<uint64_t>(128 >> 4) << 32 |             // 128 bytes between 8-row groups
                      static_cast<uint64_t>(1) << 46;                     // descriptor version for sm_100
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+  if (CTAS == 1)
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+}
+
+// ---- CTA pairs (cta_group::2) ----
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {  // one full warp of each CTA
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)), "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {  // one full warp of each CTA
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// The mbarrier at this offset in both CTAs of the pair arrives once every tcgen05 op issued so far by
+// this thread has completed.
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+// A load into this CTA's shared memory that reports to an mbarrier of either CTA of the pair (a
+// shared::cluster address).
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t bar_cluster, int c0, int c1,
+                                                 uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(c0), "r"(c1), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 // mbarrier arrives once every tcgen05 op issued so far by this thread has completed
 __device__ __forceinline__ void mma_commit(uint64_t* bar) {
