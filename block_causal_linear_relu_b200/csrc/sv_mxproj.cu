@@ -129,25 +129,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_wait();  // the previous kernel may still write the operands or read the outputs
   if (threadIdx.x == 0) griddep_launch_dependents();
 
-  if (warp == 0) {
-    if (lane == 0) {  // copies
-      const uint64_t pol_a = policy_evict_first();
-      const uint64_t pol_b = policy_evict_last();  // W is read by every row tile
-      int it = 0;
-      bool ok = true;
-      for (int tile = first; tile < g.tiles && ok; tile += step) {
-        const int m = tile / g.nt, n0 = (tile - m * g.nt) * NT;
-        const int ma = m * CTAS + rank;  // this CTA's 128 rows
-        for (int kc = 0; kc < g.runs; ++kc, ++it) {
-          const int s = it % C::kStages;
-          if (!mbar_wait(&empty[s], ((it / C::kStages) & 1) ^ 1, status, 0x6100u | s)) {
-            ok = false;
-            break;
-          }
-          uint8_t* sa = smem + s * C::kStride;
-          uint8_t* sb = sa + C::kABytes;
-          uint8_t* sc = sb + C::kBBytes;
-          const int ta = (ma * g.runs + kc) * C::kTiles;
+  // Warps 0 and 1 run their loops warp-uniformly and let one lane issue: with the loops inside a one-lane
+  // branch every operand of every instruction passed through a vector register, about 65 cycles each.
+  if (warp == 0) {  // copies
+    const uint64_t pol_a = policy_evict_first();
+    const uint64_t pol_b = policy_evict_last();  // W is read by every row tile
+    const bool issue = elect_one();
+    int s = 0;
+    uint32_t phase = 1;  // of `empty`: the first pass over the ring finds it free
+    bool ok = true;
+    for (int tile = first; tile < g.tiles && ok; tile += step) {
+      const int m = tile / g.nt, n0 = (tile - m * g.nt) * NT;
+      const int ma = m * CTAS + rank;  // this CTA's 128 rows
+      int ta = ma * g.runs * C::kTiles;
+      int tb = n0 / 128 * g.runs * C::kTiles;
+      for (int kc = 0; kc < g.runs; ++kc, ta += C::kTiles, tb += C::kTiles) {
+        if (!warp_all(mbar_wait(&empty[s], phase, status, 0x6100u | s))) {
+          ok = false;
+          break;
+        }
+        uint8_t* sa = smem + s * C::kStride;
+        uint8_t* sb = sa + C::kABytes;
+        uint8_t* sc = sb + C::kBBytes;
+        if (issue) {
           if (CTAS == 1) {
             mbar_expect_tx(&full[s], C::kStageBytes);
             tma_load_2d(sa, &maps.a, &full[s], kc * 128, ma * kRows, pol_a);
@@ -155,8 +159,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_2d(sc, &maps.sa, &full[s], 0, ta, pol_a);
 #pragma unroll
             for (int j = 0; j < C::kBBlocks; ++j)
-              tma_load_2d(sc + (1 + j) * C::kScaleBytes, &maps.sb, &full[s], 0,
-                          ((n0 / 128 + j) * g.runs + kc) * C::kTiles, pol_b);
+              tma_load_2d(sc + (1 + j) * C::kScaleBytes, &maps.sb, &full[s], 0, tb + j * g.runs * C::kTiles, pol_b);
           } else {
             const uint32_t bar = mapa_shared(smem_u32(&full[s]), 0);
             if (rank == 0) mbar_expect_tx(&full[s], 2 * C::kStageBytes);
@@ -165,34 +168,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_2d_pair(sc, &maps.sa, bar, 0, ta, pol_a);
 #pragma unroll
             for (int j = 0; j < C::kBBlocks; ++j)  // both CTAs need the scales of all NT columns
-              tma_load_2d_pair(sc + (1 + j) * C::kScaleBytes, &maps.sb, bar, 0,
-                               ((n0 / 128 + j) * g.runs + kc) * C::kTiles, pol_b);
+              tma_load_2d_pair(sc + (1 + j) * C::kScaleBytes, &maps.sb, bar, 0, tb + j * g.runs * C::kTiles, pol_b);
           }
         }
+        __syncwarp();
+        if (++s == C::kStages) s = 0, phase ^= 1;
       }
-      // the last runs' MMAs report to this CTA's barriers: stay until they have
-      for (int i = it < C::kStages ? 0 : it - C::kStages; i < it && ok; ++i)
-        ok = mbar_wait(&empty[i % C::kStages], (i / C::kStages) & 1, status, 0x6180u | (i % C::kStages));
     }
-  } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {  // scales and MMAs
-      int it = 0, tl = 0;
+    // the last runs' MMAs report to this CTA's barriers: stay until they have (a slot never used is free)
+    for (int i = 0; i < C::kStages && ok; ++i) {
+      ok = warp_all(mbar_wait(&empty[s], phase, status, 0x6180u | s));
+      if (++s == C::kStages) s = 0, phase ^= 1;
+    }
+  } else if (warp == 1) {  // scales and MMAs
+    if (rank == 0) {
+      const bool issue = elect_one();
+      int s = 0, tl = 0;
+      uint32_t phase = 0, buf = 0;
       bool ok = true;
       for (int tile = first; tile < g.tiles && ok; tile += step, ++tl) {
         const int a = tl & 1;
-        if (!mbar_wait(&acce[a], ((tl >> 1) & 1) ^ 1, status, 0x6300u | a)) break;
-        tc_fence_after();
+        if (!warp_all(mbar_wait(&acce[a], ((tl >> 1) & 1) ^ 1, status, 0x6300u | a))) break;
         const uint32_t d = tmem + static_cast<uint32_t>(a * NT);
         const int n0 = (tile % g.nt) * NT;
         const uint32_t shift = static_cast<uint32_t>(n0 % 128) / 32;  // columns of B's first scale block before the tile
-        for (int kc = 0; kc < g.runs; ++kc, ++it) {
-          const int s = it % C::kStages;
-          if (!mbar_wait(&full[s], (it / C::kStages) & 1, status, 0x6310u | s)) {
-            ok = false;
-            break;
-          }
-          // the MMAs that read this buffer of scales two runs ago have retired
-          if (it >= 2 && !mbar_wait(&empty[(it - 2) % C::kStages], ((it - 2) / C::kStages) & 1, status, 0x6320u | s)) {
+        for (int kc = 0; kc < g.runs; ++kc) {
+          if (!warp_all(mbar_wait(&full[s], phase, status, 0x6310u | s))) {
             ok = false;
             break;
           }
@@ -200,34 +201,42 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t sa = smem_u32(smem + s * C::kStride);
           const uint32_t sb = sa + C::kABytes;
           const uint32_t sc = sb + C::kBBytes;
-          const uint32_t ta = tmem + C::kScaleCol + static_cast<uint32_t>(it & 1) * C::kScaleCols;
+          const uint64_t da = sdesc_sw128(sa, 16, 1024), db = sdesc_sw128(sb, 16, 1024), ds = sdesc_scales(sc);
+          // Copies and MMAs of one thread run in order, so a copy into a buffer follows the MMAs that
+          // read it; two buffers let it run beside the MMAs of the run before.
+          const uint32_t ta = tmem + C::kScaleCol + buf * C::kScaleCols;
           const uint32_t tb = ta + 4 * C::kTiles;
+          if (issue) {
 #pragma unroll
-          for (int t = 0; t < C::kTiles; ++t) {
-            tmem_copy_scales<CTAS>(ta + 4 * t, sc + 512 * t);
+            for (int t = 0; t < C::kTiles; ++t) {
+              tmem_copy_scales<CTAS>(ta + 4 * t, ds + 32 * t);
 #pragma unroll
-            for (int j = 0; j < C::kBBlocks; ++j)
-              tmem_copy_scales<CTAS>(tb + 4 * (t * C::kBBlocks + j), sc + (1 + j) * C::kScaleBytes + 512 * t);
+              for (int j = 0; j < C::kBBlocks; ++j)
+                tmem_copy_scales<CTAS>(tb + 4 * (t * C::kBBlocks + j), ds + ((1 + j) * C::kScaleBytes >> 4) + 32 * t);
+            }
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              // step kk (32 bytes on): scale tile t, byte id of its 32-bit cells
+              const int t = FMT == SV_NVFP4 ? kk : FMT == SV_MXFP4 ? kk >> 1 : 0;
+              const uint32_t id = FMT == SV_NVFP4 ? 0 : FMT == SV_MXFP4 ? (kk & 1) * 2 : kk;
+              mma_mx<CTAS, C::kKind>(d, da + 2 * kk, db + 2 * kk,
+                                     idesc_mx(kRows * CTAS, NT, FMT == SV_MXFP8 ? 0 : 1, FMT != SV_NVFP4, id), ta + 4 * t,
+                                     tb + 4 * C::kBBlocks * t + shift, (kc | kk) != 0 ? 1u : 0u);
+            }
+            if (CTAS == 1)
+              mma_commit(&empty[s]);
+            else
+              mma_commit_pair(&empty[s]);
+            if (kc == g.runs - 1) {
+              if (CTAS == 1)
+                mma_commit(&accf[a]);
+              else
+                mma_commit_pair(&accf[a]);
+            }
           }
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            // step kk: scale tile t, byte id of its 32-bit cells
-            const int t = FMT == SV_NVFP4 ? kk : FMT == SV_MXFP4 ? kk >> 1 : 0;
-            const uint32_t id = FMT == SV_NVFP4 ? 0 : FMT == SV_MXFP4 ? (kk & 1) * 2 : kk;
-            mma_mx<CTAS, C::kKind>(d, sdesc_sw128(sa + kk * 32, 16, 1024), sdesc_sw128(sb + kk * 32, 16, 1024),
-                                   idesc_mx(kRows * CTAS, NT, FMT == SV_MXFP8 ? 0 : 1, FMT != SV_NVFP4, id), ta + 4 * t,
-                                   tb + 4 * C::kBBlocks * t + shift, (kc | kk) != 0 ? 1u : 0u);
-          }
-          if (CTAS == 1)
-            mma_commit(&empty[s]);
-          else
-            mma_commit_pair(&empty[s]);
-        }
-        if (ok) {
-          if (CTAS == 1)
-            mma_commit(&accf[a]);
-          else
-            mma_commit_pair(&accf[a]);
+          __syncwarp();
+          buf ^= 1;
+          if (++s == C::kStages) s = 0, phase ^= 1;
         }
       }
     }

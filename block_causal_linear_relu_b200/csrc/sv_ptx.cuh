@@ -210,14 +210,16 @@ __device__ __forceinline__ void mma_mx(uint32_t d_tmem, uint64_t adesc, uint64_t
   }
 }
 #undef SV_MMA_MX
-// 512 bytes of scales (32 rows of 16 bytes) from shared memory to four TMEM columns, repeated in the
-// four 32-lane quarters; ordered before the MMAs that this thread issues afterwards. CTAS = 2: each CTA of
+// Shared-memory descriptor of a 512-byte scale tile (32 rows of 16 bytes, no swizzle).
+__device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) |
+         static_cast<uint64_t>(128 >> 4) << 32 |  // 128 bytes between 8-row groups
+         static_cast<uint64_t>(1) << 46;          // descriptor version for sm_100
+}
+// A scale tile from shared memory to four TMEM columns, repeated in the four 32-lane quarters; ordered before the MMAs that this thread issues afterwards. CTAS = 2: each CTA of
 // the pair copies from its own shared memory to its own TMEM, at the same offsets.
 template <int CTAS>
-__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint32_t saddr) {
-  const uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) |  // no swizzle
-                     static_cast<uint64_t>(128 >> 4) << 32 |             // 128 bytes between 8-row groups
-                     static_cast<uint64_t>(1) << 46;                     // descriptor version for sm_100
+__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t d) {
   if (CTAS == 1)
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
   else
@@ -379,6 +381,14 @@ __device__ __forceinline__ void cluster_wait_acquire() {
 }
 // Orders this thread's generic-proxy view of memory (all state spaces) with the async proxy.
 __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+// True in one lane of a converged warp. Code before it runs warp-uniformly, so that the operands of the
+// tensor-core and copy instructions that the lane then issues are in uniform registers already.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}\n" : "=r"(p));
+  return p != 0;
+}
 
 __device__ __forceinline__ uint32_t elect_one_lane() { return (threadIdx.x & 31u) == 0u; }
 
