@@ -22,6 +22,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdio>
 #include <mutex>
 
@@ -33,7 +34,8 @@ namespace sv {
 namespace {
 
 constexpr int kRows = 128;          // rows of A per CTA
-constexpr int kThreads = 192;       // warp 0 copies, warp 1 MMAs, warps 2-5 epilogue
+constexpr int kEpiWarps = 8;        // two per 32-lane quarter of TMEM, which share its column chunks
+constexpr int kThreads = 64 + 32 * kEpiWarps;  // warp 0 copies, warp 1 MMAs, then the epilogue
 constexpr int kStaging = 32 * 128;  // per epilogue warp: 32 rows x 64 bf16
 
 template <int FMT, int CTAS, int NT>
@@ -45,16 +47,21 @@ struct Cfg {
   static constexpr int kBBytes = NT / CTAS * 128;
   static constexpr int kStageBytes = kABytes + kBBytes + (1 + kBBlocks) * kScaleBytes;
   static constexpr int kStride = (kStageBytes + 1023) / 1024 * 1024;  // the swizzle's alignment
-  static constexpr int kFit = (226 * 1024 - 4 * kStaging - 1536) / kStride;
+  static constexpr int kFit = (227 * 1024 - kEpiWarps * kStaging - 256 - 1024) / kStride;
   static constexpr int kStages = kFit < 8 ? kFit : 8;
   static constexpr int kStagingOff = kStages * kStride;
-  static constexpr int kBarOff = kStagingOff + 4 * kStaging;
+  static constexpr int kBarOff = kStagingOff + kEpiWarps * kStaging;
   static constexpr int kSmem = kBarOff + 256 + 1024;  // barriers, TMEM slot, alignment slack
   static_assert(kSmem <= 227 * 1024 && kStages >= 4, "shared memory of the microscaled product");
-  // TMEM columns: two accumulators of NT, then two buffers of scales (A: 4 per tile, B: 4 per tile and block)
+  // TMEM columns: two accumulators of NT, then two buffers of scales (A: 4 per tile, B: 4 per tile and
+  // block). Two accumulators of 256 and the scales do not fit side by side, so the second one starts inside
+  // the first: the epilogue reads the shared columns first, and the next tile may start once it has.
   static constexpr uint32_t kScaleCols = 4 * kTiles * (1 + kBBlocks);
-  static constexpr uint32_t kScaleCol = 2 * NT;
+  static constexpr bool kOverlap = 2 * NT + 2 * kScaleCols > 512;
+  static constexpr uint32_t kAcc1 = kOverlap ? (512 - NT - 2 * kScaleCols) / 32 * 32 : NT;
+  static constexpr uint32_t kScaleCol = kAcc1 + NT;
   static_assert(kScaleCol + 2 * kScaleCols <= 512, "TMEM columns");
+  static_assert(!kOverlap || (NT == 256 && kAcc1 >= 128), "the first round of the epilogue covers the shared columns");
   static constexpr MxKind kKind = FMT == SV_MXFP8 ? kMx8 : FMT == SV_MXFP4 ? kMx4 : kNv4;
 };
 
@@ -102,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&accf[a], 1);
-      mbar_init(&acce[a], 4 * CTAS);
+      mbar_init(&acce[a], kEpiWarps * CTAS);
     }
     fence_mbar_init();
     prefetch_tmap(&maps.a);
@@ -188,8 +195,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int tile = first; tile < g.tiles && ok; tile += step, ++tl) {
         const int a = tl & 1;
-        if (!warp_all(mbar_wait(&acce[a], ((tl >> 1) & 1) ^ 1, status, 0x6300u | a))) break;
-        const uint32_t d = tmem + static_cast<uint32_t>(a * NT);
+        // separate accumulators: this one's last tile (two ago) is drained; overlapping ones: the last
+        // tile's shared columns are (and then the tile before it entirely)
+        const int e = C::kOverlap ? tl - 1 : tl - 2;
+        if (e >= 0 && !warp_all(mbar_wait(&acce[e & 1], (e >> 1) & 1, status, 0x6300u | a))) break;
+        const uint32_t d = tmem + static_cast<uint32_t>(a) * C::kAcc1;
         const int n0 = (tile % g.nt) * NT;
         const uint32_t shift = static_cast<uint32_t>(n0 % 128) / 32;  // columns of B's first scale block before the tile
         for (int kc = 0; kc < g.runs; ++kc) {
@@ -241,10 +251,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {  // epilogue: warp w drains TMEM lanes 32 * (w % 4) .. + 31 (rows of this CTA's half)
-    const int q = warp & 3;
+    const int q = warp & 3, half = (warp - 2) >> 2;
     uint8_t* stg = smem + C::kStagingOff + (warp - 2) * kStaging;
     const float alpha = FMT == SV_NVFP4 ? *op.ga * *op.gb : 1.f;
     const int sub = lane >> 3, piece = lane & 7;  // store step i: row 4 i + sub, 16-byte piece of its 128 bytes
+    constexpr int kChunks = NT / 64, kRounds = (kChunks + 1) / 2;
     int tl = 0;
     for (int tile = first; tile < g.tiles; tile += step, ++tl) {
       const int a = tl & 1;
@@ -252,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const int m = tile / g.nt, n0 = (tile - m * g.nt) * NT;
       const int row0 = (m * CTAS + rank) * kRows + q * 32;
-      const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(a * NT);
+      const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(a) * C::kAcc1;
       size_t at[8];  // element offsets of the rows that this lane stores
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -265,12 +276,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
 #pragma unroll 1
-      for (int c = 0; c < NT / 64; ++c) {
+      for (int round = 0; round < kRounds; ++round) {
+        // the quarter's two warps take neighbouring chunks; overlapping accumulators: the shared columns first
+        const int c = C::kOverlap && a == 0 ? kChunks - 1 - half - 2 * round : 2 * round + half;
         uint32_t rr[2][32];
-        tmem_ld_x32(ta + c * 64, rr[0]);
-        tmem_ld_x32(ta + c * 64 + 32, rr[1]);
-        tmem_wait_ld();
-        if (c == NT / 64 - 1) {  // the tile's last TMEM read: the accumulator is free
+        if (c < kChunks) {
+          tmem_ld_x32(ta + c * 64, rr[0]);
+          tmem_ld_x32(ta + c * 64 + 32, rr[1]);
+          tmem_wait_ld();
+        }
+        if (round == (C::kOverlap ? 0 : kRounds - 1)) {  // the next user's columns are read
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
@@ -281,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const int nc = n0 + c * 64;  // first output feature of the chunk
-        if (nc >= g.nout) continue;
+        if (c >= kChunks || nc >= g.nout) continue;
         __nv_bfloat16* out = op.o0;
         bool relu = false;
         size_t base = static_cast<size_t>(nc);
@@ -403,12 +418,16 @@ sv_status run(const sv_mx& x, const sv_mx& w, const Ops& op, Geo g, void* ws, in
 template <int FMT, bool kQKV>
 sv_status choose(const sv_mx& x, const sv_mx& w, const Ops& op, const Geo& g, void* ws, int sms, cudaStream_t st) {
   if (x.rows <= 128) return run<FMT, 1, 64, kQKV>(x, w, op, g, ws, sms, st);
-  // the column tile whose last wave wastes less: waves times columns
-  const auto cost = [&](int nt) {
+  // The column tile with the least cycles: waves of tiles, a run of K taking 2 cycles per column on the
+  // tensor cores or its bytes at about 68 per cycle into an SM, whichever is more.
+  const auto cost = [&](int nt, int bytes) {
     const long long tiles = (x.rows + 255) / 256 * ((w.rows + nt - 1) / nt);
-    return (tiles + sms / 2 - 1) / (sms / 2) * nt;
+    return (tiles + sms / 2 - 1) / (sms / 2) * (static_cast<long long>(g.runs) * std::max(2 * nt, bytes / 68) + 700);
   };
-  if (cost(128) < cost(192)) return run<FMT, 2, 128, kQKV>(x, w, op, g, ws, sms, st);
+  const long long c128 = cost(128, Cfg<FMT, 2, 128>::kStageBytes), c192 = cost(192, Cfg<FMT, 2, 192>::kStageBytes),
+                  c256 = cost(256, Cfg<FMT, 2, 256>::kStageBytes);
+  if (c256 <= c192 && c256 <= c128) return run<FMT, 2, 256, kQKV>(x, w, op, g, ws, sms, st);
+  if (c128 < c192) return run<FMT, 2, 128, kQKV>(x, w, op, g, ws, sms, st);
   return run<FMT, 2, 192, kQKV>(x, w, op, g, ws, sms, st);
 }
 
