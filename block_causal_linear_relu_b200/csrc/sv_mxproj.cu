@@ -77,6 +77,7 @@ struct Geo {
 struct Maps {
   CUtensorMap a, b;    // codes: [rows, bytes], boxes of 128 rows (A) or NT / CTAS rows (B) x 128 bytes
   CUtensorMap sa, sb;  // scale tiles: [tiles, 512 bytes], boxes of a run's tiles
+  CUtensorMap o[3];    // outputs (CTA pairs): y as [rows, features], or q, k, v as [B, H, N, D]; boxes of 32 rows x 64
 };
 
 struct Ops {
@@ -264,17 +265,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int m = tile / g.nt, n0 = (tile - m * g.nt) * NT;
       const int row0 = (m * CTAS + rank) * kRows + q * 32;
       const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(a) * C::kAcc1;
-      size_t at[8];  // element offsets of the rows that this lane stores
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = row0 + 4 * i + sub;
-        if (kQKV) {
-          const int b = r / g.N;
-          at[i] = (static_cast<size_t>(b) * g.H * g.N + (r - b * g.N)) * g.D;
-        } else {
-          at[i] = static_cast<size_t>(r) * g.nout;
-        }
-      }
+      const int b0 = kQKV ? row0 / g.N : 0, tok0 = kQKV ? row0 - b0 * g.N : row0;
+      // one bulk store takes the warp's 32 rows, unless they run into the next batch
+      const bool bulk = CTAS == 2 && (!kQKV || tok0 + 32 <= g.N);
 #pragma unroll 1
       for (int round = 0; round < kRounds; ++round) {
         // the quarter's two warps take neighbouring chunks; overlapping accumulators: the shared columns first
@@ -297,14 +290,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int nc = n0 + c * 64;  // first output feature of the chunk
         if (c >= kChunks || nc >= g.nout) continue;
-        __nv_bfloat16* out = op.o0;
-        bool relu = false;
-        size_t base = static_cast<size_t>(nc);
-        if (kQKV) {
-          const int hd = g.H * g.D, t = nc / hd, f = nc - t * hd, h = f / g.D;
-          out = t == 0 ? op.o0 : (t == 1 ? op.o1 : op.o2);
-          relu = t < 2;
-          base = static_cast<size_t>(h) * g.N * g.D + (f - h * g.D);
+        const int hd = kQKV ? g.H * g.D : g.nout;
+        const int t = kQKV ? nc / hd : 0, f = nc - t * hd;  // tensor, feature in it
+        const int h = kQKV ? f / g.D : 0, d0 = kQKV ? f - h * g.D : f;
+        const bool relu = kQKV && t < 2;
+        if (CTAS == 2) {  // the last bulk store has read the buffer
+          if (lane == 0) bulk_wait_read_all();
+          __syncwarp();
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -317,17 +309,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           *reinterpret_cast<uint4*>(stg + lane * 128 + ((j ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        __syncwarp();
-        const bool col_ok = nc + piece * 8 < g.nout;
+        if (bulk) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && row0 < g.rows) {
+            tma_store_4d(&maps.o[t], stg, d0, tok0, h, b0);
+            bulk_commit();
+          }
+          __syncwarp();
+        } else {
+          __syncwarp();
+          __nv_bfloat16* out = t == 0 ? op.o0 : (t == 1 ? op.o1 : op.o2);
+          const bool col_ok = nc + piece * 8 < g.nout;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = 4 * i + sub;
-          const uint4 w = *reinterpret_cast<const uint4*>(stg + r * 128 + ((piece ^ (r & 7)) << 4));
-          if (col_ok && row0 + r < g.rows) *reinterpret_cast<uint4*>(out + at[i] + base + piece * 8) = w;
+          for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + sub;
+            const uint4 w = *reinterpret_cast<const uint4*>(stg + r * 128 + ((piece ^ (r & 7)) << 4));
+            const int b = kQKV ? (row0 + r) / g.N : 0;
+            const size_t at = kQKV ? ((static_cast<size_t>(b) * g.H + h) * g.N + (row0 + r - b * g.N)) * g.D + d0
+                                   : static_cast<size_t>(row0 + r) * g.nout + d0;
+            if (col_ok && row0 + r < g.rows) *reinterpret_cast<uint4*>(out + at + piece * 8) = w;
+          }
         }
         __syncwarp();
       }
     }
+    if (CTAS == 2 && lane == 0) bulk_wait_all();
   }
   tc_fence_before();
   __syncthreads();
@@ -392,6 +399,20 @@ sv_status run(const sv_mx& x, const sv_mx& w, const Ops& op, Geo g, void* ws, in
   MXP_TRY(encode_bytes_2d(&maps.b, w.codes, bytes, static_cast<uint64_t>(w.rows), NT / CTAS));
   MXP_TRY(encode_scale_tiles(&maps.sa, x.scales, static_cast<uint64_t>(sa), C::kTiles));
   MXP_TRY(encode_scale_tiles(&maps.sb, w.scales, static_cast<uint64_t>(sb), C::kTiles));
+  if (CTAS == 2) {
+    const uint32_t box[4] = {64, 32, 1, 1};
+    if (kQKV) {
+      const uint64_t D = static_cast<uint64_t>(g.D), N = static_cast<uint64_t>(g.N), H = static_cast<uint64_t>(g.H);
+      const uint64_t dims[4] = {D, N, H, static_cast<uint64_t>(x.rows) / N}, pitch[3] = {2 * D, 2 * N * D, 2 * H * N * D};
+      MXP_TRY(encode_bf16_4d(&maps.o[0], op.o0, dims, pitch, box));
+      MXP_TRY(encode_bf16_4d(&maps.o[1], op.o1, dims, pitch, box));
+      MXP_TRY(encode_bf16_4d(&maps.o[2], op.o2, dims, pitch, box));
+    } else {
+      const uint64_t F = static_cast<uint64_t>(g.nout), R = static_cast<uint64_t>(x.rows);
+      const uint64_t dims[4] = {F, R, 1, 1}, pitch[3] = {2 * F, 2 * R * F, 2 * R * F};
+      MXP_TRY(encode_bf16_4d(&maps.o[0], op.o0, dims, pitch, box));
+    }
+  }
   cudaError_t e = ensure_attr<FMT, CTAS, NT, kQKV>();
   if (e == cudaSuccess) {
     const int groups = sms / CTAS;
