@@ -53,15 +53,12 @@ struct Cfg {
   static constexpr int kBarOff = kStagingOff + kEpiWarps * kStaging;
   static constexpr int kSmem = kBarOff + 256 + 1024;  // barriers, TMEM slot, alignment slack
   static_assert(kSmem <= 227 * 1024 && kStages >= 4, "shared memory of the microscaled product");
-  // TMEM columns: two accumulators of NT, then two buffers of scales (A: 4 per tile, B: 4 per tile and
-  // block). Two accumulators of 256 and the scales do not fit side by side, so the second one starts inside
-  // the first: the epilogue reads the shared columns first, and the next tile may start once it has.
+  // TMEM columns: the accumulators (two of up to 192 columns; two of 256 and the scales do not fit), then two
+  // buffers of scales (A: 4 per tile, B: 4 per tile and block)
   static constexpr uint32_t kScaleCols = 4 * kTiles * (1 + kBBlocks);
-  static constexpr bool kOverlap = 2 * NT + 2 * kScaleCols > 512;
-  static constexpr uint32_t kAcc1 = kOverlap ? (512 - NT - 2 * kScaleCols) / 32 * 32 : NT;
-  static constexpr uint32_t kScaleCol = kAcc1 + NT;
+  static constexpr int kAccs = 2 * NT + 2 * kScaleCols <= 512 ? 2 : 1;
+  static constexpr uint32_t kScaleCol = kAccs * NT;
   static_assert(kScaleCol + 2 * kScaleCols <= 512, "TMEM columns");
-  static_assert(!kOverlap || (NT == 256 && kAcc1 >= 128), "the first round of the epilogue covers the shared columns");
   static constexpr MxKind kKind = FMT == SV_MXFP8 ? kMx8 : FMT == SV_MXFP4 ? kMx4 : kNv4;
 };
 
@@ -70,7 +67,7 @@ struct Geo {
   int nout;     // output features
   int runs;     // 128-byte runs of K
   int nt;       // column tiles
-  int tiles;    // all tiles, column tile fastest
+  int tiles;    // all tiles
   int N, H, D;  // Q/K/V only: tokens per batch, heads, head features
 };
 
@@ -85,6 +82,9 @@ struct Ops {
   __nv_bfloat16 *o0, *o1, *o2;  // y, or q, k, v
 };
 
+// Tiles are numbered column tile fastest: the CTAs at work share a few row tiles of A (read from DRAM once)
+// and sweep W, which stays in L2. Blocks of 4 or 8 row tiles, which touch fewer distinct tiles at a time,
+// measured 2.5 and 5 % slower on the 720p Q/K/V projection.
 __device__ __forceinline__ bool warp_all(bool ok) { return __all_sync(0xffffffffu, ok); }
 
 template <int FMT, int CTAS, int NT, bool kQKV>
@@ -195,14 +195,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0, buf = 0;
       bool ok = true;
       for (int tile = first; tile < g.tiles && ok; tile += step, ++tl) {
-        const int a = tl & 1;
-        // separate accumulators: this one's last tile (two ago) is drained; overlapping ones: the last
-        // tile's shared columns are (and then the tile before it entirely)
-        const int e = C::kOverlap ? tl - 1 : tl - 2;
-        if (e >= 0 && !warp_all(mbar_wait(&acce[e & 1], (e >> 1) & 1, status, 0x6300u | a))) break;
-        const uint32_t d = tmem + static_cast<uint32_t>(a) * C::kAcc1;
+        const int a = tl % C::kAccs;
+        const uint32_t d = tmem + static_cast<uint32_t>(a * NT);
         const int n0 = (tile % g.nt) * NT;
         const uint32_t shift = static_cast<uint32_t>(n0 % 128) / 32;  // columns of B's first scale block before the tile
+        if (!warp_all(mbar_wait(&acce[a], ((tl / C::kAccs) & 1) ^ 1, status, 0x6300u | a))) break;
         for (int kc = 0; kc < g.runs; ++kc) {
           if (!warp_all(mbar_wait(&full[s], phase, status, 0x6310u | s))) {
             ok = false;
@@ -259,35 +256,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kChunks = NT / 64, kRounds = (kChunks + 1) / 2;
     int tl = 0;
     for (int tile = first; tile < g.tiles; tile += step, ++tl) {
-      const int a = tl & 1;
-      if (!warp_all(mbar_wait(&accf[a], (tl >> 1) & 1, status, 0x6400u | a))) break;
+      const int a = tl % C::kAccs;
+      if (!warp_all(mbar_wait(&accf[a], (tl / C::kAccs) & 1, status, 0x6400u | a))) break;
       tc_fence_after();
       const int m = tile / g.nt, n0 = (tile - m * g.nt) * NT;
       const int row0 = (m * CTAS + rank) * kRows + q * 32;
-      const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(a) * C::kAcc1;
+      const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(a * NT);
       const int b0 = kQKV ? row0 / g.N : 0, tok0 = kQKV ? row0 - b0 * g.N : row0;
       // one bulk store takes the warp's 32 rows, unless they run into the next batch
       const bool bulk = CTAS == 2 && (!kQKV || tok0 + 32 <= g.N);
-#pragma unroll 1
+      // Everything this warp owns goes to registers at once, and the accumulator is free: TMEM reads stall
+      // the tensor cores (about 1700 cycles a tile when spread over the next tile's MMAs), and here all
+      // four quarters are read at the same time, with one accumulator while the MMAs wait anyway.
+      uint32_t rr[kRounds][64];
+#pragma unroll
+      for (int round = 0; round < kRounds; ++round)
+        if (2 * round + half < kChunks) tmem_ld_x64(ta + (2 * round + half) * 64, rr[round]);
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (CTAS == 1)
+          mbar_arrive(&acce[a]);
+        else
+          mbar_arrive_pair(mapa_shared(smem_u32(&acce[a]), 0));
+      }
+#pragma unroll
       for (int round = 0; round < kRounds; ++round) {
-        // the quarter's two warps take neighbouring chunks; overlapping accumulators: the shared columns first
-        const int c = C::kOverlap && a == 0 ? kChunks - 1 - half - 2 * round : 2 * round + half;
-        uint32_t rr[2][32];
-        if (c < kChunks) {
-          tmem_ld_x32(ta + c * 64, rr[0]);
-          tmem_ld_x32(ta + c * 64 + 32, rr[1]);
-          tmem_wait_ld();
-        }
-        if (round == (C::kOverlap ? 0 : kRounds - 1)) {  // the next user's columns are read
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if (CTAS == 1)
-              mbar_arrive(&acce[a]);
-            else
-              mbar_arrive_cluster(mapa_shared(smem_u32(&acce[a]), 0));
-          }
-        }
+        const int c = 2 * round + half;  // the quarter's two warps take neighbouring chunks
         const int nc = n0 + c * 64;  // first output feature of the chunk
         if (c >= kChunks || nc >= g.nout) continue;
         const int hd = kQKV ? g.H * g.D : g.nout;
@@ -300,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          const uint32_t* v = rr[j >> 2] + 8 * (j & 3);
+          const uint32_t* v = rr[round] + 8 * j;
           uint32_t w[4];
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
