@@ -462,8 +462,20 @@ def sv_block_causal_attn_rope(q, k, v, block_len: int, rope: Rope3dTable, frame0
     return o
 
 
-_MX_BLOCK = {SV_MXFP8: 32, SV_MXFP4: 32, SV_NVFP4: 16}
-_MX_RUN = {SV_MXFP8: 128, SV_MXFP4: 256, SV_NVFP4: 256}  # columns in 128 bytes of codes
+_MX_BLOCK = (32, 32, 16)     # by format: columns in a block
+_MX_RUN = (128, 256, 256)    # columns in 128 bytes of codes
+
+
+def _mx_scale_shape(rows, cols, fmt):
+    run = _MX_RUN[fmt]
+    return (-(-rows // 128), -(-cols // run) * (run // _MX_BLOCK[fmt]) // 4, 32, 4, 4)
+
+
+def _mx_sizes(rows, cols, fmt):
+    """(bytes of codes rounded up to 256, bytes of scales)."""
+    run = _MX_RUN[fmt]
+    return ((rows * cols >> (fmt != SV_MXFP8)) + 255 & -256,
+            (rows + 127 & -128) * (-(-cols // run) * (run // _MX_BLOCK[fmt])))
 
 
 class MxTensor:
@@ -474,53 +486,87 @@ class MxTensor:
     at every call: change them in place, or make another MxTensor.
     """
 
-    __slots__ = ("codes", "scales", "gscale", "rows", "cols", "fmt", "_c", "_ref")
+    __slots__ = ("_codes", "_scales", "_buf", "gscale", "rows", "cols", "fmt", "device", "_c", "_ref")
 
     def __init__(self, codes, scales, rows: int, cols: int, fmt: int, gscale=None):
-        if fmt not in _MX_BLOCK:
-            raise ValueError("fmt must be SV_MXFP8, SV_MXFP4 or SV_NVFP4")
-        if rows < 1 or cols < 32 or cols % 32 != 0:
-            raise ValueError("rows must be >= 1 and cols a positive multiple of 32")
-        dev = codes.device
+        _mx_check(rows, cols, fmt, gscale, codes.device)
         if not codes.is_cuda:
             raise ValueError("codes must live on a CUDA device")
         if codes.dtype != torch.uint8 or codes.shape != (rows, cols if fmt == SV_MXFP8 else cols // 2) or not codes.is_contiguous():
             raise ValueError("codes must be a contiguous uint8 tensor [rows, cols] (SV_MXFP8) or [rows, cols / 2]")
         if (scales.dtype != torch.uint8 or scales.shape != _mx_scale_shape(rows, cols, fmt) or not scales.is_contiguous()
-                or scales.device != dev):
+                or scales.device != codes.device):
             raise ValueError(f"scales must be a contiguous uint8 tensor {_mx_scale_shape(rows, cols, fmt)} on codes' device")
-        if (gscale is None) != (fmt != SV_NVFP4):
-            raise ValueError("SV_NVFP4 needs a tensor scale gscale; the other formats take none")
-        if gscale is not None and (gscale.dtype != torch.float32 or gscale.numel() != 1 or gscale.device != dev):
-            raise ValueError("gscale must be a float32 tensor of one value on codes' device")
-        self.codes, self.scales, self.gscale = codes, scales, gscale
-        self.rows, self.cols, self.fmt = rows, cols, fmt
-        self._c = SvMx(codes.data_ptr(), scales.data_ptr(), None if gscale is None else gscale.data_ptr(), rows, cols, fmt)
+        self._codes, self._scales, self._buf = codes, scales, None
+        self._set(rows, cols, fmt, gscale, codes.device, codes.data_ptr(), scales.data_ptr())
+
+    def _set(self, rows, cols, fmt, gscale, device, codes, scales):
+        self.rows, self.cols, self.fmt, self.gscale, self.device = rows, cols, fmt, gscale, device
+        self._c = SvMx(codes, scales, None if gscale is None else gscale.data_ptr(), rows, cols, fmt)
         self._ref = ctypes.byref(self._c)
 
     @classmethod
     def empty(cls, rows: int, cols: int, fmt: int, gscale=None, device=None):
         """An MxTensor with uninitialised codes and scales (an output for sv_mx_quantize or sv_rmsnorm)."""
-        if fmt not in _MX_BLOCK:
-            raise ValueError("fmt must be SV_MXFP8, SV_MXFP4 or SV_NVFP4")
-        device = device if device is not None else (gscale.device if gscale is not None else torch.device("cuda"))
-        codes = torch.empty((rows, cols if fmt == SV_MXFP8 else cols // 2), dtype=torch.uint8, device=device)
-        scales = torch.empty(_mx_scale_shape(rows, cols, fmt), dtype=torch.uint8, device=device)
-        return cls(codes, scales, rows, cols, fmt, gscale)
+        if device is None:
+            device = gscale.device if gscale is not None else torch.device("cuda", torch.cuda.current_device())
+        else:
+            device = torch.device(device)
+        _mx_check(rows, cols, fmt, gscale, device)
+        m = cls.__new__(cls)
+        n, ns = _mx_sizes(rows, cols, fmt)  # one allocation; codes and scales are views made when asked for
+        m._codes = m._scales = None
+        m._buf = torch.empty(n + ns, dtype=torch.uint8, device=device)
+        p = m._buf.data_ptr()
+        m._set(rows, cols, fmt, gscale, m._buf.device, p, p + n)
+        return m
 
     @property
-    def device(self):
-        return self.codes.device
+    def codes(self):
+        if self._codes is None:
+            c = self.cols if self.fmt == SV_MXFP8 else self.cols // 2
+            self._codes = self._buf.as_strided((self.rows, c), (c, 1), 0)
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            shape = _mx_scale_shape(self.rows, self.cols, self.fmt)
+            n = _mx_sizes(self.rows, self.cols, self.fmt)[0]
+            self._scales = self._buf.as_strided(shape, (shape[1] * 512, 512, 16, 4, 1), n)
+        return self._scales
 
 
-def _mx_scale_shape(rows, cols, fmt):
-    run = _MX_RUN[fmt]
-    return (-(-rows // 128), -(-cols // run) * (run // _MX_BLOCK[fmt]) // 4, 32, 4, 4)
+def _mx_check(rows, cols, fmt, gscale, device):
+    if fmt not in (SV_MXFP8, SV_MXFP4, SV_NVFP4):
+        raise ValueError("fmt must be SV_MXFP8, SV_MXFP4 or SV_NVFP4")
+    if rows < 1 or cols < 32 or cols % 32 != 0:
+        raise ValueError("rows must be >= 1 and cols a positive multiple of 32")
+    if (gscale is None) != (fmt != SV_NVFP4):
+        raise ValueError("SV_NVFP4 needs a tensor scale gscale; the other formats take none")
+    if gscale is not None and (gscale.dtype != torch.float32 or gscale.numel() != 1 or gscale.device != device):
+        raise ValueError("gscale must be a float32 tensor of one value on codes' device")
 
 
-def _on_device(t):
-    """Makes t's device current for the call when it is not (a no-op context otherwise)."""
-    return torch.cuda.device(t.device)
+def _call(fn, device, stream, *args):
+    """Calls fn(*args, stream) with `device` current (the framework's tensors may live on another device
+    than the current one) and raises on an error."""
+    index = device.index
+    if index == torch.cuda.current_device():
+        st = fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
+    if st != SV_OK:
+        _check(st)
+
+
+def _raw_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):  # the same handle without a Stream object
+    _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _mx_out(out, rows, cols, fmt, gscale, device):
@@ -541,11 +587,12 @@ def _dense(x, name):
 def sv_mx_global_scale(x, g=None, stream=None):
     """The tensor scale of SV_NVFP4: max |x| / (6 * 448) as a float32 tensor [1] (g, when given)."""
     _dense(x, "x")
-    g = torch.empty(1, dtype=torch.float32, device=x.device) if g is None else g
-    if g.dtype != torch.float32 or g.numel() != 1 or g.device != x.device:
+    device = x.device
+    if g is None:
+        g = torch.empty(1, dtype=torch.float32, device=device)
+    elif g.dtype != torch.float32 or g.numel() != 1 or g.device != device:
         raise ValueError("g must be a float32 tensor of one value on x's device")
-    with _on_device(x):
-        _check(load().sv_mx_global_scale(_ptr(x), x.numel(), _dt(x), _ptr(g), _stream(stream)))
+    _call(load().sv_mx_global_scale, device, stream, x.data_ptr(), x.numel(), _dt(x), g.data_ptr())
     return g
 
 
@@ -553,26 +600,27 @@ def sv_mx_quantize(x, fmt: int, gscale=None, out: MxTensor | None = None, stream
     """x to a microscaled matrix: [..., C] rows as they are, or [B, H, N, D] (four dimensions) as B * N
     rows that hold the heads side by side. SV_NVFP4 takes the tensor scale gscale (float32 [1])."""
     _dense(x, "x")
-    if x.dim() < 2:
+    shape = x.shape
+    if len(shape) < 2:
         raise ValueError("x must be [..., C] or [B, H, N, D]")
-    if x.dim() == 4:
-        B, H, N, D = x.shape
+    if len(shape) == 4:
+        B, H, N, D = shape
     else:
-        B, H, D = 1, 1, x.shape[-1]
+        B, H, D = 1, 1, shape[-1]
         N = x.numel() // D if D else 0
-    out = _mx_out(out, B * N, H * D, fmt, gscale, x.device)
-    with _on_device(x):
-        _check(load().sv_mx_quantize(_ptr(x), B, H, N, D, _dt(x), out._ref, _stream(stream)))
+    device = x.device
+    out = _mx_out(out, B * N, H * D, fmt, gscale, device)
+    _call(load().sv_mx_quantize, device, stream, x.data_ptr(), B, H, N, D, _dt(x), out._ref)
     return out
 
 
 def sv_mx_dequantize(xq: MxTensor, dtype=torch.bfloat16, y=None, stream=None):
     """The values of a microscaled matrix as [rows, cols] bfloat16 or float32."""
-    y = torch.empty(xq.rows, xq.cols, dtype=dtype, device=xq.device) if y is None else y
-    if tuple(y.shape) != (xq.rows, xq.cols) or not y.is_contiguous() or y.device != xq.device:
+    if y is None:
+        y = torch.empty((xq.rows, xq.cols), dtype=dtype, device=xq.device)
+    elif tuple(y.shape) != (xq.rows, xq.cols) or not y.is_contiguous() or y.device != xq.device:
         raise ValueError("y must be a contiguous [rows, cols] tensor on xq's device")
-    with _on_device(y):
-        _check(load().sv_mx_dequantize(xq._ref, _ptr(y), _dt(y), _stream(stream)))
+    _call(load().sv_mx_dequantize, xq.device, stream, xq._ref, y.data_ptr(), _dt(y))
     return y
 
 
@@ -583,34 +631,35 @@ def sv_rmsnorm(x, w, residual=None, eps: float = 1e-6, fmt: int | None = None, g
     or, with fmt, quantised in the same pass to an MxTensor of one row per position (y, when given, is that
     MxTensor; SV_NVFP4 takes gscale). h may be x or residual (in place)."""
     _dense(x, "x")
-    C = x.shape[-1] if x.dim() else 0
-    if C == 0 or x.numel() == 0:
+    shape, dtype, device = x.shape, x.dtype, x.device
+    C = shape[-1] if len(shape) else 0
+    rows = x.numel() // C if C else 0
+    if rows == 0:
         raise ValueError("x must be [..., C] with at least one row and column")
-    if w.dtype != torch.float32 or tuple(w.shape) != (C,) or not w.is_contiguous() or w.device != x.device:
+    if w.dtype != torch.float32 or w.shape != (C,) or not w.is_contiguous() or w.device != device:
         raise ValueError("w must be a contiguous float32 [C] tensor on x's device")
     if residual is None:
         if h is not None and h is not x:
             raise ValueError("without a residual h is x")
         h = x
+        pr = ph = None
     else:
         h = torch.empty_like(x) if h is None else h
-    for t, name in ((residual, "residual"), (h, "h")):
-        if t is not None and t is not x and (t.shape != x.shape or t.dtype != x.dtype or t.device != x.device or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous tensor of x's shape, dtype and device")
-    rows = x.numel() // C
+        for t in (residual, h):
+            if t is not x and (t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous()):
+                raise ValueError("residual and h must be contiguous tensors of x's shape, dtype and device")
+        pr, ph = residual.data_ptr(), h.data_ptr()
     if fmt is None:
         if gscale is not None:
             raise ValueError("gscale goes with fmt=SV_NVFP4")
         y = torch.empty_like(x) if y is None else y
-        if y.shape != x.shape or y.dtype != x.dtype or y.device != x.device or not y.is_contiguous():
+        if y.shape != shape or y.dtype != dtype or y.device != device or not y.is_contiguous():
             raise ValueError("y must be a contiguous tensor of x's shape, dtype and device")
         py, pq = y.data_ptr(), None
     else:
-        y = _mx_out(y, rows, C, fmt, gscale, x.device)
+        y = _mx_out(y, rows, C, fmt, gscale, device)
         py, pq = None, y._ref
-    with _on_device(x):
-        _check(load().sv_rmsnorm(_ptr(x), _ptr(residual), None if residual is None else _ptr(h), _ptr(w), rows, C, _dt(x),
-                                 eps, py, pq, _stream(stream)))
+    _call(load().sv_rmsnorm, device, stream, x.data_ptr(), pr, ph, w.data_ptr(), rows, C, _dt(x), eps, py, pq)
     return y, h
 
 
@@ -622,7 +671,8 @@ def _mx_workspace(device, stream):
     so calls on several streams share it."""
     ws = _mx_ws.get(device.index)
     if ws is None:
-        ws = _mx_ws[device.index] = Workspace(256, device, stream)
+        with torch.cuda.device(device):
+            ws = _mx_ws[device.index] = Workspace(256, device, stream)
     ws.check(stream)
     return ws
 
@@ -636,13 +686,14 @@ def sv_mx_projection(xq: MxTensor, wq: MxTensor, y=None, ws: Workspace | None = 
     """y [xq.rows, wq.rows] bfloat16 = x W^T of two microscaled matrices. Make the first call on a device
     (or pass ws) before capturing one into a CUDA graph."""
     _mx_pair(xq, wq)
-    y = torch.empty(xq.rows, wq.rows, dtype=torch.bfloat16, device=xq.device) if y is None else y
-    if (y.dtype != torch.bfloat16 or y.numel() != xq.rows * wq.rows or y.shape[-1] != wq.rows or not y.is_contiguous()
-            or y.device != xq.device):
+    device = xq.device
+    if y is None:
+        y = torch.empty((xq.rows, wq.rows), dtype=torch.bfloat16, device=device)
+    elif (y.dtype != torch.bfloat16 or y.numel() != xq.rows * wq.rows or y.shape[-1] != wq.rows or not y.is_contiguous()
+            or y.device != device):
         raise ValueError("y must be a contiguous bfloat16 tensor of x's rows and w's rows on x's device")
-    with _on_device(y):
-        ws = ws if ws is not None else _mx_workspace(xq.device, stream)
-        _check(load().sv_mx_projection(xq._ref, wq._ref, _ptr(y), ws.ptr, ws.nbytes, _stream(stream)))
+    ws = ws if ws is not None else _mx_workspace(device, stream)
+    _call(load().sv_mx_projection, device, stream, xq._ref, wq._ref, y.data_ptr(), ws.ptr, ws.nbytes)
     return y
 
 
@@ -652,12 +703,12 @@ def sv_mx_qkv_projection(xq: MxTensor, wq: MxTensor, B: int, N: int, H: int, D: 
     sv_mx_projection."""
     _mx_pair(xq, wq)
     shape = (B, H, N, D)
-    q, k, v = (torch.empty(shape, dtype=torch.bfloat16, device=xq.device) if t is None else t for t in (q, k, v))
+    device = xq.device
+    q, k, v = (torch.empty(shape, dtype=torch.bfloat16, device=device) if t is None else t for t in (q, k, v))
     for t in (q, k, v):
-        if tuple(t.shape) != shape or t.dtype != torch.bfloat16 or not t.is_contiguous() or t.device != xq.device:
+        if t.shape != shape or t.dtype != torch.bfloat16 or not t.is_contiguous() or t.device != device:
             raise ValueError("q, k, v must be contiguous bfloat16 [B, H, N, D] tensors on x's device")
-    with _on_device(q):
-        ws = ws if ws is not None else _mx_workspace(xq.device, stream)
-        _check(load().sv_mx_qkv_projection(xq._ref, wq._ref, _ptr(q), _ptr(k), _ptr(v), B, N, H, D, ws.ptr, ws.nbytes,
-                                           _stream(stream)))
+    ws = ws if ws is not None else _mx_workspace(device, stream)
+    _call(load().sv_mx_qkv_projection, device, stream, xq._ref, wq._ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), B, N,
+          H, D, ws.ptr, ws.nbytes)
     return q, k, v
