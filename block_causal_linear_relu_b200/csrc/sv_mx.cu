@@ -2,18 +2,18 @@
 // back, the tensor scale, and the root-mean-square norm whose output is quantised in the same pass.
 //
 // All of it is bound by HBM: a pass reads each input once and writes codes and scales once. A thread
-// holds 16 consecutive columns in registers (one SV_NVFP4 block, half an MX block whose other half
-// sits in the neighbouring lane), so a block's largest magnitude takes at most one shuffle.
+// holds octets of columns in registers (16 bytes of bf16: coalesced loads and stores), and a block is two
+// (SV_NVFP4) or four neighbouring lanes, so its largest magnitude takes one or two shuffles.
 //
 // Rounding. An element is x / s (or x / (s g)) rounded once, to nearest even. For the MX formats s is
 // a power of two and the product x * 2^-k is exact, so the conversion instruction rounds correctly.
-// For SV_NVFP4 the quotient q = x * fp32(1 / fp32(s g)) is off by at most about 2^-22 relative; when
-// q (1 - 2^-20) and q (1 + 2^-20) convert to the same code no border lies between them and that code is
-// the answer. Otherwise (bf16 inputs and a measured g do lie on borders) |x| is compared with the
-// exact borders t * s * g, products of 3 + 4 + 24 bits, in fp64. The scale's quotient a / (6 g) is
-// taken in fp64 (its distance from a border of e4m3 is at least 2^-33 relative, unless it lies on it)
-// and goes to fp32 towards zero with the lost bits or-ed into the lowest one, so that the second
-// rounding, to e4m3, gives what a single one would.
+// For SV_NVFP4 the fp32 quotients q (of an element, x * fp32(1 / fp32(s g)), and of the scale, a * fp32(1 /
+// fp32(6 g))) are off by at most about 2^-22 relative; when q (1 - 2^-20) and q (1 + 2^-20) convert to the
+// same code no border lies between them and that code is the answer. Otherwise (bf16 inputs and a
+// measured g do lie on borders) it is found exactly: |x| is compared with the borders t * s * g, products
+// of 3 + 4 + 24 bits, in fp64; the scale's quotient a / (6 g) is taken in fp64 (its distance from a border
+// of e4m3 is at least 2^-33 relative, unless it lies on it) and goes to fp32 towards zero with the lost
+// bits or-ed into the lowest one, so that the second rounding, to e4m3, gives what a single one would.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -29,16 +29,20 @@
 namespace sv {
 namespace {
 
-constexpr int kGroup = 16;       // columns per thread
+constexpr int kOct = 8;           // columns per lane and step: 16 bytes of bf16
 constexpr int kMxThreads = 256;  // threads of the quantising and dequantising kernels
+constexpr int kUnroll = 4;       // octets per thread there, all loaded before the first is used
 
-// ---- loads and stores of 16 columns, in two 8-column halves (16-byte aligned) ----
+// ---- eight columns as loaded (16-byte aligned) ----
 template <typename T>
-struct Half;
+struct Oct;
 template <>
-struct Half<__nv_bfloat16> {
-  static __device__ __forceinline__ void load(const __nv_bfloat16* p, float* f) {
-    const uint4 r = *reinterpret_cast<const uint4*>(p);
+struct Oct<__nv_bfloat16> {
+  uint4 r;
+  __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { r = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = r; }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
     const uint32_t u[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -46,27 +50,29 @@ struct Half<__nv_bfloat16> {
       f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
     }
   }
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* f) {
-    uint4 r;
-    r.x = pack_bf16x2(f[0], f[1]);
-    r.y = pack_bf16x2(f[2], f[3]);
-    r.z = pack_bf16x2(f[4], f[5]);
-    r.w = pack_bf16x2(f[6], f[7]);
-    *reinterpret_cast<uint4*>(p) = r;
+  __device__ __forceinline__ void set(const float (&f)[8]) {  // rounded
+    r = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
   }
-  static __device__ __forceinline__ float round(float f) { return __bfloat162float(__float2bfloat16_rn(f)); }
 };
 template <>
-struct Half<float> {
-  static __device__ __forceinline__ void load(const float* p, float* f) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+struct Oct<float> {
+  float4 a, b;
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void store(float* p) const {
+    reinterpret_cast<float4*>(p)[0] = a;
+    reinterpret_cast<float4*>(p)[1] = b;
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
     f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
   }
-  static __device__ __forceinline__ void store(float* p, const float* f) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  __device__ __forceinline__ void set(const float (&f)[8]) {
+    a = make_float4(f[0], f[1], f[2], f[3]);
+    b = make_float4(f[4], f[5], f[6], f[7]);
   }
-  static __device__ __forceinline__ float round(float f) { return f; }
 };
 
 // ---- conversions ----
@@ -135,14 +141,6 @@ __device__ __forceinline__ float pow2f_bits(int k) {
 
 constexpr uint32_t kInfBits = 0x7f800000u;
 
-// the bits of max |f_i|; infinities and NaN compare above every finite value
-__device__ __forceinline__ uint32_t amax_bits(const float (&f)[kGroup]) {
-  uint32_t a = 0;
-#pragma unroll
-  for (int i = 0; i < kGroup; ++i) a = max(a, __float_as_uint(f[i]) & 0x7fffffffu);
-  return a;
-}
-
 // Eight elements of SV_NVFP4 by the exact borders: code of |x| = how many borders t * d lie below it,
 // a border itself going to the even code.
 __device__ __forceinline__ uint32_t e2m1_exact(float x, double d) {
@@ -163,64 +161,78 @@ static __device__ __noinline__ uint32_t e2m1x8_exact(float f0, float f1, float f
          e2m1_exact(f4, d) << 16 | e2m1_exact(f5, d) << 20 | e2m1_exact(f6, d) << 24 | e2m1_exact(f7, d) << 28;
 }
 
-// One thread's 16 columns to codes (SV_MXFP8: four words, else two) and the block's scale byte.
-// Every lane of the warp calls it (the MX formats pair lanes 2i and 2i + 1).
+// The scale of a block of SV_NVFP4 from the quotient in fp64 (see the top of the file).
+static __device__ __noinline__ uint32_t e4m3_exact(float a, float g) {
+  const double ratio = fmin(static_cast<double>(a) / (6.0 * static_cast<double>(g)), 448.0);
+  float rz = __double2float_rz(ratio);
+  if (static_cast<double>(rz) != ratio) rz = __uint_as_float(__float_as_uint(rz) | 1u);
+  const float z4[4] = {rz, 0.f, 0.f, 0.f};
+  return cvt_e4m3x4(z4) & 0xffu;
+}
+
+// What a thread needs to know about the tensor scale.
+struct TensorScale {
+  float g, inv6g;
+  bool finite, fits;  // fits: the fp32 quotients keep their accuracy
+};
+__device__ __forceinline__ TensorScale tensor_scale(float g) {
+  return {g, 1.0f / (6.0f * g), g - g == 0.0f, g > 0x1p-90f && g < 0x1p90f};
+}
+
+// One lane's eight columns to codes (SV_MXFP8: two words, else one) and the block's scale byte. Every lane
+// of the warp calls it: a block is two neighbouring lanes (SV_NVFP4) or four.
 template <int FMT>
-__device__ __forceinline__ uint32_t quantise16(const float (&f)[kGroup], float g, uint32_t (&code)[4]) {
-  uint32_t ab = amax_bits(f);
+__device__ __forceinline__ uint32_t quantise8(const float (&f)[8], const TensorScale& ts, uint32_t (&code)[2]) {
+  uint32_t ab = 0;  // bits of max |f_i|; infinities and NaN compare above every finite value
+#pragma unroll
+  for (int i = 0; i < 8; ++i) ab = max(ab, __float_as_uint(f[i]) & 0x7fffffffu);
+  ab = max(ab, __shfl_xor_sync(0xffffffffu, ab, 1));
+  code[1] = 0u;
   if (FMT == SV_NVFP4) {
-    if (ab >= kInfBits || !(fabsf(g) < __uint_as_float(kInfBits))) {
-      code[0] = code[1] = 0u;
+    if (ab >= kInfBits || !ts.finite) {
+      code[0] = 0u;
       return 0x7fu;  // NaN
     }
-    const double gd = static_cast<double>(g);
-    const double ratio = static_cast<double>(__uint_as_float(ab)) / (6.0 * gd);
-    float rz = __double2float_rz(fmin(ratio, 448.0));
-    if (static_cast<double>(rz) != fmin(ratio, 448.0)) rz = __uint_as_float(__float_as_uint(rz) | 1u);
-    float z4[4] = {rz, 0.f, 0.f, 0.f};
-    const uint32_t sb = cvt_e4m3x4(z4) & 0xffu;
+    const float a = __uint_as_float(ab);
+    const float t = a * ts.inv6g;
+    const float two[4] = {t * (1.0f - 0x1p-20f), t * (1.0f + 0x1p-20f), 0.f, 0.f};
+    const uint32_t c2 = cvt_e4m3x4(two);
+    uint32_t sb = c2 & 0xffu;
+    if (!ts.fits || sb != c2 >> 8) sb = e4m3_exact(a, ts.g);
     const float s = e4m3_to_f32(sb);
-    const float d = s * g;
-    if (!(s > 0.f) || !(gd > 0.0)) {
-      code[0] = code[1] = 0u;
+    if (!(s > 0.f) || !(ts.g > 0.f)) {
+      code[0] = 0u;
       return sb;
     }
-    const bool fits = d > 0x1p-100f && d < 0x1p100f;  // the fp32 quotient keeps its accuracy
-    const float r = fits ? 1.0f / d : 0.f;
+    const float r = 1.0f / (s * ts.g);
+    float lo[8], hi[8];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float lo[8], hi[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float q = f[8 * h + i] * r;
-        lo[i] = q * (1.0f - 0x1p-20f);
-        hi[i] = q * (1.0f + 0x1p-20f);
-      }
-      const uint32_t c = cvt_e2m1x8(lo);
-      code[h] = c;
-      if (!fits || c != cvt_e2m1x8(hi)) {
-        const float* v = f + 8 * h;
-        code[h] = e2m1x8_exact(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7], static_cast<double>(s) * gd);
-      }
+    for (int i = 0; i < 8; ++i) {
+      const float q = f[i] * r;
+      lo[i] = q * (1.0f - 0x1p-20f);
+      hi[i] = q * (1.0f + 0x1p-20f);
     }
+    code[0] = cvt_e2m1x8(lo);
+    if (!ts.fits || code[0] != cvt_e2m1x8(hi))
+      code[0] = e2m1x8_exact(f[0], f[1], f[2], f[3], f[4], f[5], f[6], f[7],
+                             static_cast<double>(s) * static_cast<double>(ts.g));
     return sb;
   } else {
-    ab = max(ab, __shfl_xor_sync(0xffffffffu, ab, 1));
+    ab = max(ab, __shfl_xor_sync(0xffffffffu, ab, 2));
     // a = m 2^k, 1 <= m < 2; the largest element is 1.75 * 2^8 (e4m3) or 1.5 * 2^2 (e2m1)
     const uint32_t top = FMT == SV_MXFP8 ? 0x600000u : 0x400000u;
     int k = static_cast<int>(ab >> 23) - 127 - (FMT == SV_MXFP8 ? 8 : 2) + ((ab & 0x7fffffu) > top ? 1 : 0);
     k = max(k, -127);
     const bool bad = ab >= kInfBits;
-    const float r = bad ? 0.f : pow2f_bits(-k);
-    float q[kGroup];
+    const float r = pow2f_bits(bad ? 0 : -k);
+    float q[8];
 #pragma unroll
-    for (int i = 0; i < kGroup; ++i) q[i] = f[i] * r;
+    for (int i = 0; i < 8; ++i) q[i] = f[i] * r;
     if (FMT == SV_MXFP8) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) code[i] = bad ? 0u : cvt_e4m3x4(q + 4 * i);
+      code[0] = bad ? 0u : cvt_e4m3x4(q);
+      code[1] = bad ? 0u : cvt_e4m3x4(q + 4);
     } else {
       code[0] = bad ? 0u : cvt_e2m1x8(q);
-      code[1] = bad ? 0u : cvt_e2m1x8(q + 8);
     }
     return bad ? 0xffu : static_cast<uint32_t>(k + 127);
   }
@@ -232,99 +244,129 @@ __device__ __forceinline__ size_t scale_at(size_t row, int blk, int sp) {
          ((row >> 5) & 3) * 4 + (blk & 3);
 }
 
-// Writes one thread's codes (when `live`: it holds real columns) and, when `in` (it holds a place of the
-// scale tiles), its scale byte, four blocks of a row to a 32-bit store: the padded groups of a row are a
-// whole number of four-block words, so the lanes that hold a word's blocks belong to one row. Every
-// lane of the warp calls it.
+// Writes one lane's codes (when `live`: it holds real columns) and, when `in` (it holds a place of the scale
+// tiles), its block's scale byte, four blocks of a row to a 32-bit store: the padded octets of a row
+// are a whole number of four-block words, so the lanes that hold a word's blocks belong to one row.
+// Every lane of the warp calls it.
 template <int FMT>
-__device__ __forceinline__ void put16(uint8_t* codes, uint8_t* scales, size_t row, int grp, int cols, int sp, bool in,
-                                      bool live, const uint32_t (&code)[4], uint32_t sb) {
-  constexpr int kPer = FMT == SV_NVFP4 ? 1 : 2;  // groups per block
-  const int blk = grp / kPer;
-  uint32_t w = sb << (8 * (blk & 3));
-  if (kPer == 1) w |= __shfl_xor_sync(0xffffffffu, w, 1);
-  w |= __shfl_xor_sync(0xffffffffu, w, 2);
-  if (kPer == 2) w |= __shfl_xor_sync(0xffffffffu, w, 4);
-  if (in && grp % (4 * kPer) == 0) *reinterpret_cast<uint32_t*>(scales + scale_at(row, blk, sp)) = w;
+__device__ __forceinline__ void put8(uint8_t* codes, uint8_t* scales, size_t row, int oct, int cols, int sp, bool in,
+                                     bool live, const uint32_t (&code)[2], uint32_t sb) {
+  constexpr int kPer = FMT == SV_NVFP4 ? 2 : 4;  // octets per block
+  const int blk = oct / kPer;
+  uint32_t w = live ? sb << (8 * (blk & 3)) : 0u;
+  w |= __shfl_xor_sync(0xffffffffu, w, kPer);
+  w |= __shfl_xor_sync(0xffffffffu, w, 2 * kPer);
+  if (in && oct % (4 * kPer) == 0) *reinterpret_cast<uint32_t*>(scales + scale_at(row, blk, sp)) = w;
   if (!live) return;
   if (FMT == SV_MXFP8)
-    *reinterpret_cast<uint4*>(codes + row * cols + static_cast<size_t>(grp) * 16) =
-        make_uint4(code[0], code[1], code[2], code[3]);
+    *reinterpret_cast<uint2*>(codes + row * cols + static_cast<size_t>(oct) * 8) = make_uint2(code[0], code[1]);
   else
-    *reinterpret_cast<uint2*>(codes + row * (cols / 2) + static_cast<size_t>(grp) * 8) = make_uint2(code[0], code[1]);
+    *reinterpret_cast<uint32_t*>(codes + row * (cols / 2) + static_cast<size_t>(oct) * 4) = code[0];
 }
 
-// One thread per (padded row, padded group): rows rounded up to 128 and gp groups per row (a multiple
-// of 8), so every warp is full and the places of the scale tiles that hold no block are written too.
-template <int FMT, typename T>
+// A block's threads take kUnroll octets each of the (padded row, padded octet) grid, kMxThreads apart: rows
+// rounded up to 128 and op octets per row (a multiple of 16), so every warp is full and the places of the
+// scale tiles that hold no block are written too. step_rows, step_oct: kMxThreads octets in rows and octets.
+struct Walk {
+  uint32_t row;
+  int oct;
+  __device__ __forceinline__ Walk(size_t idx, uint32_t op)
+      : row(static_cast<uint32_t>(idx / op)), oct(static_cast<int>(idx - static_cast<size_t>(row) * op)) {}
+  __device__ __forceinline__ void next(uint32_t step_rows, int step_oct, int op) {
+    row += step_rows;
+    oct += step_oct;
+    if (oct >= op) oct -= op, ++row;
+  }
+};
+
+template <int FMT, typename T, bool kHeads>
 __global__ void __launch_bounds__(kMxThreads) quantize_kernel(const T* __restrict__ x, int H, int N, int D, uint32_t rows,
-                                                              int cols, int gp, int sp, const float* gscale,
-                                                              uint8_t* codes, uint8_t* scales) {
+                                                              int cols, int op, int step_rows, int step_oct, int sp,
+                                                              uint32_t rows_padded, const float* gscale, uint8_t* codes,
+                                                              uint8_t* scales) {
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
-  const size_t idx = static_cast<size_t>(blockIdx.x) * kMxThreads + threadIdx.x;
-  const uint32_t row = static_cast<uint32_t>(idx / static_cast<uint32_t>(gp));
-  const int grp = static_cast<int>(idx - static_cast<size_t>(row) * gp);
-  const bool live = row < rows && grp * kGroup < cols;
-  float f[kGroup];
+  Walk at(static_cast<size_t>(blockIdx.x) * (kMxThreads * kUnroll) + threadIdx.x, static_cast<uint32_t>(op));
+  Oct<T> v[kUnroll];
+  {
+    Walk w = at;
 #pragma unroll
-  for (int i = 0; i < kGroup; ++i) f[i] = 0.f;
-  if (live) {
-    const int c = grp * kGroup;
-    if (H == 1) {
-      const T* p = x + static_cast<size_t>(row) * cols + c;
-      Half<T>::load(p, f);
-      Half<T>::load(p + 8, f + 8);
-    } else {
-      const uint32_t b = row / static_cast<uint32_t>(N), n = row - b * static_cast<uint32_t>(N);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int head = (c + 8 * h) / D, d = c + 8 * h - head * D;
-        Half<T>::load(x + ((static_cast<size_t>(b) * H + head) * N + n) * D + d, f + 8 * h);
+    for (int u = 0; u < kUnroll; ++u) {
+      const int c = w.oct * kOct;
+      size_t from;
+      if (kHeads) {
+        const uint32_t b = w.row / static_cast<uint32_t>(N), n = w.row - b * static_cast<uint32_t>(N);
+        const uint32_t head = static_cast<uint32_t>(c) / static_cast<uint32_t>(D);
+        from = ((static_cast<size_t>(b) * H + head) * N + n) * D + (c - head * D);
+      } else {
+        from = static_cast<size_t>(w.row) * cols + c;
       }
+      v[u].zero();
+      if (w.row < rows && c < cols) v[u].load(x + from);
+      w.next(step_rows, step_oct, op);
     }
   }
-  uint32_t code[4];
-  uint32_t sb = quantise16<FMT>(f, FMT == SV_NVFP4 ? *gscale : 1.f, code);
-  put16<FMT>(codes, scales, row, grp, cols, sp, true, live, code, live ? sb : 0u);
+  const TensorScale ts = tensor_scale(FMT == SV_NVFP4 ? *gscale : 1.f);
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    float f[8];
+    v[u].get(f);
+    uint32_t code[2];
+    const uint32_t sb = quantise8<FMT>(f, ts, code);
+    put8<FMT>(codes, scales, at.row, at.oct, cols, sp, at.row < rows_padded, at.row < rows && at.oct * kOct < cols, code,
+              sb);
+    at.next(step_rows, step_oct, op);
+  }
 }
 
-// One thread per (row, group): value = element * scale (exact in fp32) * g, rounded once to T.
+// value = element * scale (exact in fp32) * g, rounded once to T; kUnroll octets of the (row, octet) grid
+// per thread.
 template <int FMT, typename T>
 __global__ void __launch_bounds__(kMxThreads) dequantize_kernel(const uint8_t* __restrict__ codes,
                                                                 const uint8_t* __restrict__ scales, const float* gscale,
-                                                                int cols, int sp, T* y, size_t total) {
+                                                                int op, int step_rows, int step_oct, int sp, T* y,
+                                                                size_t total) {
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
-  const size_t idx = static_cast<size_t>(blockIdx.x) * kMxThreads + threadIdx.x;
-  if (idx >= total) return;
-  const uint32_t gpr = static_cast<uint32_t>(cols) / kGroup;
-  const uint32_t row = static_cast<uint32_t>(idx / gpr);
-  const int grp = static_cast<int>(idx - static_cast<size_t>(row) * gpr);
-  const uint32_t sb = scales[scale_at(row, FMT == SV_NVFP4 ? grp : grp >> 1, sp)];
-  float f[kGroup];
-  if (FMT == SV_MXFP8) {
-    const uint4 c = *reinterpret_cast<const uint4*>(codes + idx * 16);
-    e4m3x4_to_f32(c.x, f);
-    e4m3x4_to_f32(c.y, f + 4);
-    e4m3x4_to_f32(c.z, f + 8);
-    e4m3x4_to_f32(c.w, f + 12);
-  } else {
-    const uint2 c = *reinterpret_cast<const uint2*>(codes + idx * 8);
-    e2m1x8_to_f32(c.x, f);
-    e2m1x8_to_f32(c.y, f + 8);
-  }
-  float s, g = 1.f;
-  if (FMT == SV_NVFP4) {
-    s = e4m3_to_f32(sb);
-    g = *gscale;
-  } else {
-    s = sb == 255u ? __uint_as_float(0x7fffffffu) : pow2f_bits(static_cast<int>(sb) - 127);
-  }
+  size_t idx = static_cast<size_t>(blockIdx.x) * (kMxThreads * kUnroll) + threadIdx.x;
+  Walk at(idx, static_cast<uint32_t>(op));
+  uint2 c[kUnroll];
+  uint32_t sb[kUnroll];
 #pragma unroll
-  for (int i = 0; i < kGroup; ++i) f[i] = f[i] * s * g;
-  Half<T>::store(y + idx * kGroup, f);
-  Half<T>::store(y + idx * kGroup + 8, f + 8);
+  for (int u = 0; u < kUnroll; ++u) {
+    const size_t i = idx + static_cast<size_t>(u) * kMxThreads;
+    c[u] = make_uint2(0, 0);
+    sb[u] = 0;
+    if (i < total) {
+      if (FMT == SV_MXFP8)
+        c[u] = *reinterpret_cast<const uint2*>(codes + i * 8);
+      else
+        c[u].x = *reinterpret_cast<const uint32_t*>(codes + i * 4);
+      sb[u] = scales[scale_at(at.row, at.oct / (FMT == SV_NVFP4 ? 2 : 4), sp)];
+    }
+    at.next(step_rows, step_oct, op);
+  }
+  const float g = FMT == SV_NVFP4 ? *gscale : 1.f;
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const size_t i = idx + static_cast<size_t>(u) * kMxThreads;
+    if (i >= total) break;
+    float f[8];
+    if (FMT == SV_MXFP8) {
+      e4m3x4_to_f32(c[u].x, f);
+      e4m3x4_to_f32(c[u].y, f + 4);
+    } else {
+      e2m1x8_to_f32(c[u].x, f);
+    }
+    const float s = FMT == SV_NVFP4 ? e4m3_to_f32(sb[u])
+                    : sb[u] == 255u ? __uint_as_float(0x7fffffffu)
+                                    : pow2f_bits(static_cast<int>(sb[u]) - 127);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = f[j] * s * g;
+    Oct<T> o;
+    o.set(f);
+    o.store(y + i * kOct);
+  }
 }
 
 // *g = max over the grid of max |x_i| / 2688. The quotient of non-negative values grows with |x|, so
@@ -337,7 +379,9 @@ __global__ void __launch_bounds__(kMxThreads) global_scale_kernel(const T* __res
   for (size_t i = (static_cast<size_t>(blockIdx.x) * kMxThreads + threadIdx.x) * 8; i < n; i += step) {
     float f[8];
     if (i + 8 <= n) {
-      Half<T>::load(x + i, f);
+      Oct<T> v;
+      v.load(x + i);
+      v.get(f);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[j] = i + j < n ? static_cast<float>(x[i + j]) : 0.f;
@@ -358,10 +402,12 @@ __global__ void __launch_bounds__(kMxThreads) global_scale_kernel(const T* __res
 
 // ---- norm ----
 // A team of blockDim.x threads takes one row (blockDim.y rows per block; more than one only with
-// one-warp teams). Thread t holds the groups i * blockDim.x + t, i < G, in registers from the load to
-// the store, so x and the residual are read once. Squares are summed in fp64: then 1 / sqrt(mean + eps),
-// rounded to fp32, does not depend on how the row is split over threads (but for one case in about 1e8),
-// and quantised outputs, where a last-bit difference can move an element by a whole step, do not either.
+// one-warp teams). Thread t holds the octets i * blockDim.x + t, i < O, in registers from the load to the
+// store, so x and the residual are read once; all loads are issued before the first is used (with the
+// unpacked values in registers and loads between their uses the 720p prefill took 292 us, bound by their
+// latency). Squares are summed in fp64: then 1 / sqrt(mean + eps), rounded to fp32, does not depend on how
+// the row is split over threads (but for one case in about 1e8), and quantised outputs, where a last-bit
+// difference can move an element by a whole step, do not either.
 constexpr int kPlain = -1;
 constexpr int kMaxTeam = 512;
 
@@ -371,11 +417,10 @@ __device__ __forceinline__ double warp_sum(double v) {
   return v;
 }
 
-template <int FMT, typename T, int G>
-__global__ void __launch_bounds__(G == 1 || G == 4 ? kMaxTeam : 256) rmsnorm_kernel(const T* x, const T* res, T* h_out, const float* __restrict__ w,
-                                                           size_t rows, size_t rows_padded, int cols, int gp, int sp,
-                                                           float eps, T* y, const float* gscale, uint8_t* codes,
-                                                           uint8_t* scales) {
+template <int FMT, typename T, int O>
+__global__ void __launch_bounds__(O == 1 || O == 8 ? kMaxTeam : 256)
+    rmsnorm_kernel(const T* x, const T* res, T* h_out, const float* __restrict__ w, size_t rows, size_t rows_padded,
+                   int cols, int op, int sp, float eps, T* y, const float* gscale, uint8_t* codes, uint8_t* scales) {
   __shared__ double part[kMaxTeam / 32];
   griddep_wait();
   if (threadIdx.x == 0 && threadIdx.y == 0) griddep_launch_dependents();
@@ -383,37 +428,49 @@ __global__ void __launch_bounds__(G == 1 || G == 4 ? kMaxTeam : 256) rmsnorm_ker
   if (row >= rows_padded) return;  // whole warps: with blockDim.y == 1 the whole block
   const int team = blockDim.x;
   const bool real = row < rows;
-  float f[G][kGroup];
-  double sum = 0.0;
+  const size_t base = row * cols;
+  Oct<T> h[O];
+  {
+    Oct<T> r[O];
 #pragma unroll
-  for (int i = 0; i < G; ++i) {
-    const int c = (i * team + static_cast<int>(threadIdx.x)) * kGroup;
+    for (int i = 0; i < O; ++i) {
+      const int c = (i * team + static_cast<int>(threadIdx.x)) * kOct;
+      h[i].zero();
+      if (real && c < cols) h[i].load(x + base + c);
+    }
+    if (res != nullptr) {
 #pragma unroll
-    for (int j = 0; j < kGroup; ++j) f[i][j] = 0.f;
-    if (!real) continue;
+      for (int i = 0; i < O; ++i) {
+        const int c = (i * team + static_cast<int>(threadIdx.x)) * kOct;
+        r[i].zero();
+        if (real && c < cols) r[i].load(res + base + c);
+      }
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const int c8 = c + 8 * hf;
-      if (c8 >= cols) continue;
-      float* v = f[i] + 8 * hf;
-      const size_t at = row * cols + c8;
-      Half<T>::load(x + at, v);
-      if (res != nullptr) {
-        float r[8];
-        Half<T>::load(res + at, r);
+      for (int i = 0; i < O; ++i) {
+        float f[8], q[8];
+        h[i].get(f);
+        r[i].get(q);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = Half<T>::round(v[j] + r[j]);
+        for (int j = 0; j < 8; ++j) f[j] += q[j];
+        h[i].set(f);
       }
     }
   }
+  double s0 = 0.0, s1 = 0.0;
 #pragma unroll
-  for (int i = 0; i < G; ++i)
+  for (int i = 0; i < O; ++i) {
+    float f[8];
+    h[i].get(f);
 #pragma unroll
-    for (int j = 0; j < kGroup; ++j) {
-      const double d = f[i][j];
-      sum = fma(d, d, sum);
+    for (int j = 0; j < 8; j += 2) {
+      const double a = f[j], b = f[j + 1];
+      s0 = fma(a, a, s0);
+      s1 = fma(b, b, s1);
     }
-  sum = warp_sum(sum);
+    const int c = (i * team + static_cast<int>(threadIdx.x)) * kOct;
+    if (h_out != nullptr && real && c < cols) h[i].store(h_out + base + c);
+  }
+  double sum = warp_sum(s0 + s1);
   if (team > 32) {
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
     __syncthreads();
@@ -421,31 +478,31 @@ __global__ void __launch_bounds__(G == 1 || G == 4 ? kMaxTeam : 256) rmsnorm_ker
     for (int k = 0; k < team / 32; ++k) sum += part[k];
   }
   const float rstd = static_cast<float>(1.0 / sqrt(sum / cols + static_cast<double>(eps)));
-  const float g = FMT == SV_NVFP4 ? *gscale : 1.f;
+  const TensorScale ts = tensor_scale(FMT == SV_NVFP4 ? *gscale : 1.f);
 #pragma unroll
-  for (int i = 0; i < G; ++i) {
-    const int grp = i * team + static_cast<int>(threadIdx.x);
-    const int c = grp * kGroup;
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const int c8 = c + 8 * hf;
-      if (!real || c8 >= cols) continue;
-      float* v = f[i] + 8 * hf;
-      const size_t at = row * cols + c8;
-      if (h_out != nullptr) Half<T>::store(h_out + at, v);
-      const float4 w0 = __ldg(reinterpret_cast<const float4*>(w + c8)), w1 = __ldg(reinterpret_cast<const float4*>(w + c8) + 1);
+  for (int i = 0; i < O; ++i) {
+    const int oct = i * team + static_cast<int>(threadIdx.x);
+    const int c = oct * kOct;
+    const bool live = real && c < cols;
+    float f[8];
+    h[i].get(f);
+    if (live) {
+      const float4 w0 = __ldg(reinterpret_cast<const float4*>(w + c)), w1 = __ldg(reinterpret_cast<const float4*>(w + c) + 1);
       const float ww[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = v[j] * rstd * ww[j];
-      if (FMT == kPlain) Half<T>::store(y + at, v);
+      for (int j = 0; j < 8; ++j) f[j] = f[j] * rstd * ww[j];
     }
-    if (FMT != kPlain) {
+    if (FMT == kPlain) {
+      if (live) {
+        Oct<T> o;
+        o.set(f);
+        o.store(y + base + c);
+      }
+    } else {
       constexpr int F = FMT == kPlain ? 0 : FMT;
-      const bool live = real && c < cols;
-      uint32_t code[4];
-      const uint32_t sb = quantise16<F>(f[i], g, code);
-      // the team may cover more groups than the padded row has
-      put16<F>(codes, scales, row, grp, cols, sp, grp < gp, live, code, live ? sb : 0u);
+      uint32_t code[2];
+      const uint32_t sb = quantise8<F>(f, ts, code);
+      put8<F>(codes, scales, row, oct, cols, sp, oct < op, live, code, sb);  // the team may cover more than op octets
     }
   }
 }
@@ -499,27 +556,33 @@ sv_status mx_size(sv_mx_format fmt, long long rows, int cols) {
 template <int FMT, typename T>
 sv_status run_quantize(const void* x, int H, int N, int D, const sv_mx& m, cudaStream_t st) {
   const int sp = mx_padded_blocks(m.fmt, m.cols);
-  const int gp = sp * mx_block(m.fmt) / kGroup;
-  const long long blocks = mx_row_tiles(m.rows) * 128 * gp / kMxThreads;
+  const int op = sp * mx_block(m.fmt) / kOct;
+  const long long rows_padded = mx_row_tiles(m.rows) * 128, per = kMxThreads * kUnroll;
+  const long long blocks = (rows_padded * op + per - 1) / per;
   if (blocks > 0x7fffffffLL) return mfail(SV_ERR_UNSUPPORTED, "too many elements");
   cudaLaunchAttribute at;
   const cudaLaunchConfig_t cfg = pdl_config(dim3(static_cast<unsigned>(blocks)), dim3(kMxThreads), st, &at);
-  return launched(cudaLaunchKernelEx(&cfg, quantize_kernel<FMT, T>, static_cast<const T*>(x), H, N, D,
-                                     static_cast<uint32_t>(m.rows), m.cols, gp, sp, m.gscale,
-                                     static_cast<uint8_t*>(m.codes), static_cast<uint8_t*>(m.scales)),
-                  "quantisation");
+  const auto go = [&](auto kernel) {
+    return launched(cudaLaunchKernelEx(&cfg, kernel, static_cast<const T*>(x), H, N, D, static_cast<uint32_t>(m.rows),
+                                       m.cols, op, kMxThreads / op, kMxThreads % op, sp,
+                                       static_cast<uint32_t>(rows_padded), m.gscale, static_cast<uint8_t*>(m.codes),
+                                       static_cast<uint8_t*>(m.scales)),
+                    "quantisation");
+  };
+  return H == 1 ? go(quantize_kernel<FMT, T, false>) : go(quantize_kernel<FMT, T, true>);
 }
 
 template <int FMT, typename T>
 sv_status run_dequantize(const sv_mx& m, void* y, cudaStream_t st) {
-  const size_t total = static_cast<size_t>(m.rows) * (m.cols / kGroup);
-  const size_t blocks = (total + kMxThreads - 1) / kMxThreads;
+  const int op = m.cols / kOct;
+  const size_t total = static_cast<size_t>(m.rows) * op, per = kMxThreads * kUnroll;
+  const size_t blocks = (total + per - 1) / per;
   if (blocks > 0x7fffffffull) return mfail(SV_ERR_UNSUPPORTED, "too many elements");
   cudaLaunchAttribute at;
   const cudaLaunchConfig_t cfg = pdl_config(dim3(static_cast<unsigned>(blocks)), dim3(kMxThreads), st, &at);
   return launched(cudaLaunchKernelEx(&cfg, dequantize_kernel<FMT, T>, static_cast<const uint8_t*>(m.codes),
-                                     static_cast<const uint8_t*>(m.scales), m.gscale, m.cols,
-                                     mx_padded_blocks(m.fmt, m.cols), static_cast<T*>(y), total),
+                                     static_cast<const uint8_t*>(m.scales), m.gscale, op, kMxThreads / op,
+                                     kMxThreads % op, mx_padded_blocks(m.fmt, m.cols), static_cast<T*>(y), total),
                   "dequantisation");
 }
 
@@ -534,33 +597,33 @@ struct NormArgs {
   const sv_mx* q;
 };
 
-template <int FMT, typename T, int G>
-sv_status launch_norm(const NormArgs& a, int team, int gp, int sp, cudaStream_t st) {
+template <int FMT, typename T, int O>
+sv_status launch_norm(const NormArgs& a, int team, int op, int sp, cudaStream_t st) {
   const int per_block = team == 32 ? 8 : 1;
   const long long rows_padded = a.q != nullptr ? mx_row_tiles(a.rows) * 128 : a.rows;
   const long long blocks = (rows_padded + per_block - 1) / per_block;
   cudaLaunchAttribute at;
   const cudaLaunchConfig_t cfg = pdl_config(dim3(static_cast<unsigned>(blocks)), dim3(team, per_block), st, &at);
   return launched(
-      cudaLaunchKernelEx(&cfg, rmsnorm_kernel<FMT, T, G>, static_cast<const T*>(a.x), static_cast<const T*>(a.res),
+      cudaLaunchKernelEx(&cfg, rmsnorm_kernel<FMT, T, O>, static_cast<const T*>(a.x), static_cast<const T*>(a.res),
                          static_cast<T*>(a.h), a.w, static_cast<size_t>(a.rows), static_cast<size_t>(rows_padded), a.C,
-                         gp, sp, a.eps, static_cast<T*>(a.y), a.q != nullptr ? a.q->gscale : nullptr,
+                         op, sp, a.eps, static_cast<T*>(a.y), a.q != nullptr ? a.q->gscale : nullptr,
                          a.q != nullptr ? static_cast<uint8_t*>(a.q->codes) : nullptr,
                          a.q != nullptr ? static_cast<uint8_t*>(a.q->scales) : nullptr),
       "norm");
 }
 
 template <int FMT, typename T>
-sv_status run_norm(const NormArgs& a, cudaStream_t st) {
+sv_status run_norm(const NormArgs& a, int sms, cudaStream_t st) {
   const int sp = a.q != nullptr ? mx_padded_blocks(a.q->fmt, a.C) : 0;
-  const int gp = a.q != nullptr ? sp * mx_block(a.q->fmt) / kGroup : (a.C + kGroup - 1) / kGroup;
-  // one warp to a row while its groups fit five to a lane; a whole block beyond that
-  if (gp <= 32) return launch_norm<FMT, T, 1>(a, 32, gp, sp, st);
-  if (gp <= 64) return launch_norm<FMT, T, 2>(a, 32, gp, sp, st);
-  if (gp <= 160) return launch_norm<FMT, T, 5>(a, 32, gp, sp, st);
-  const int team = gp <= 512 ? (gp + 31) / 32 * 32 : 512;
-  if (gp <= 512) return launch_norm<FMT, T, 1>(a, team, gp, sp, st);
-  return launch_norm<FMT, T, 4>(a, team, gp, sp, st);
+  const int op = a.q != nullptr ? sp * mx_block(a.q->fmt) / kOct : (a.C + kOct - 1) / kOct;
+  // Few rows: a thread per octet, so that a row's latency is one load's and a short sum's. Many: one warp
+  // to a row while its octets fit ten to a lane, a block of eight octets per thread beyond that.
+  if (a.rows <= 4 * sms && op <= kMaxTeam) return launch_norm<FMT, T, 1>(a, (op + 31) / 32 * 32, op, sp, st);
+  if (op <= 64) return launch_norm<FMT, T, 2>(a, 32, op, sp, st);
+  if (op <= 160) return launch_norm<FMT, T, 5>(a, 32, op, sp, st);
+  if (op <= 320) return launch_norm<FMT, T, 10>(a, 32, op, sp, st);
+  return launch_norm<FMT, T, 8>(a, ((op + 7) / 8 + 31) / 32 * 32, op, sp, st);
 }
 
 // Calls f<FMT, T>(args...) for a runtime format and type.
@@ -702,6 +765,6 @@ extern "C" sv_status sv_rmsnorm(const void* x, const void* residual, void* h, co
   const NormArgs a{x, residual, residual == nullptr && h == x ? nullptr : h, w, rows, C, eps, y, yq};
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (yq == nullptr)
-    return dt == SV_BF16 ? run_norm<kPlain, __nv_bfloat16>(a, st) : run_norm<kPlain, float>(a, st);
-  MX_DISPATCH(yq->fmt, dt, run_norm, a, st);
+    return dt == SV_BF16 ? run_norm<kPlain, __nv_bfloat16>(a, sms, st) : run_norm<kPlain, float>(a, sms, st);
+  MX_DISPATCH(yq->fmt, dt, run_norm, a, sms, st);
 }
