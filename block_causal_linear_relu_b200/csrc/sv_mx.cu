@@ -29,9 +29,10 @@
 namespace sv {
 namespace {
 
-constexpr int kOct = 8;           // columns per lane and step: 16 bytes of bf16
+constexpr int kOct = 8;           // columns per lane and step: 16 bytes of bf16 (norm and values)
+constexpr int kGroup = 16;        // columns per lane and step where they are quantised
 constexpr int kMxThreads = 256;  // threads of the quantising and dequantising kernels
-constexpr int kUnroll = 4;       // octets per thread there, all loaded before the first is used
+constexpr int kUnroll = 2;       // steps per thread there, all loaded before the first is used
 
 // ---- eight columns as loaded (16-byte aligned) ----
 template <typename T>
@@ -72,6 +73,32 @@ struct Oct<float> {
   __device__ __forceinline__ void set(const float (&f)[8]) {
     a = make_float4(f[0], f[1], f[2], f[3]);
     b = make_float4(f[4], f[5], f[6], f[7]);
+  }
+};
+
+// E columns (8 or 16) as loaded
+template <typename T, int E>
+struct Cols {
+  Oct<T> o[E / 8];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < E / 8; ++i) o[i].zero();
+  }
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < E / 8; ++i) o[i].load(p + 8 * i);
+  }
+  __device__ __forceinline__ void store(T* p) const {
+#pragma unroll
+    for (int i = 0; i < E / 8; ++i) o[i].store(p + 8 * i);
+  }
+  __device__ __forceinline__ void get(float (&f)[E]) const {
+#pragma unroll
+    for (int i = 0; i < E / 8; ++i) o[i].get(*reinterpret_cast<float(*)[8]>(f + 8 * i));
+  }
+  __device__ __forceinline__ void set(const float (&f)[E]) {
+#pragma unroll
+    for (int i = 0; i < E / 8; ++i) o[i].set(*reinterpret_cast<const float(*)[8]>(f + 8 * i));
   }
 };
 
@@ -179,18 +206,42 @@ __device__ __forceinline__ TensorScale tensor_scale(float g) {
   return {g, 1.0f / (6.0f * g), g - g == 0.0f, g > 0x1p-90f && g < 0x1p90f};
 }
 
-// One lane's eight columns to codes (SV_MXFP8: two words, else one) and the block's scale byte. Every lane
-// of the warp calls it: a block is two neighbouring lanes (SV_NVFP4) or four.
-template <int FMT>
-__device__ __forceinline__ uint32_t quantise8(const float (&f)[8], const TensorScale& ts, uint32_t (&code)[2]) {
-  uint32_t ab = 0;  // bits of max |f_i|; infinities and NaN compare above every finite value
+// The bits of max |f_i| over 16 columns, in fp32; infinities and NaN compare above every finite value.
+__device__ __forceinline__ uint32_t amax16(const float (&f)[16]) {
+  float a = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) ab = max(ab, __float_as_uint(f[i]) & 0x7fffffffu);
-  ab = max(ab, __shfl_xor_sync(0xffffffffu, ab, 1));
-  code[1] = 0u;
+  for (int i = 0; i < 16; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(fabsf(f[i])));
+  return __float_as_uint(a);
+}
+// The same of 16 columns as loaded.
+__device__ __forceinline__ uint32_t amax16(const Cols<__nv_bfloat16, 16>& v) {
+  // pairs of 15-bit magnitudes, ordered as integers
+  uint32_t a = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    a = __vmaxu2(a, v.o[i].r.x & 0x7fff7fffu);
+    a = __vmaxu2(a, v.o[i].r.y & 0x7fff7fffu);
+    a = __vmaxu2(a, v.o[i].r.z & 0x7fff7fffu);
+    a = __vmaxu2(a, v.o[i].r.w & 0x7fff7fffu);
+  }
+  return max(a << 16, a & 0xffff0000u);
+}
+__device__ __forceinline__ uint32_t amax16(const Cols<float, 16>& v) {
+  float f[16];
+  v.get(f);
+  return amax16(f);
+}
+
+// One lane's 16 columns, whose largest magnitude has the bits amax, to codes (SV_MXFP8: four words, else
+// two) and the block's scale byte: a block of SV_NVFP4, or half a block of the MX formats, whose lanes 2i
+// and 2i + 1 both have it. Every lane of the warp calls it.
+template <int FMT>
+__device__ __forceinline__ uint32_t quantise16(const float (&f)[16], uint32_t amax, const TensorScale& ts,
+                                               uint32_t (&code)[4]) {
+  uint32_t ab = amax;
   if (FMT == SV_NVFP4) {
     if (ab >= kInfBits || !ts.finite) {
-      code[0] = 0u;
+      code[0] = code[1] = 0u;
       return 0x7fu;  // NaN
     }
     const float a = __uint_as_float(ab);
@@ -201,38 +252,44 @@ __device__ __forceinline__ uint32_t quantise8(const float (&f)[8], const TensorS
     if (!ts.fits || sb != c2 >> 8) sb = e4m3_exact(a, ts.g);
     const float s = e4m3_to_f32(sb);
     if (!(s > 0.f) || !(ts.g > 0.f)) {
-      code[0] = 0u;
+      code[0] = code[1] = 0u;
       return sb;
     }
-    const float r = 1.0f / (s * ts.g);
-    float lo[8], hi[8];
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(s * ts.g));  // off by 2^-23 at most
+    const float rl = r * (1.0f - 0x1p-20f), rh = r * (1.0f + 0x1p-20f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float q = f[i] * r;
-      lo[i] = q * (1.0f - 0x1p-20f);
-      hi[i] = q * (1.0f + 0x1p-20f);
+    for (int h = 0; h < 2; ++h) {
+      const float* v = f + 8 * h;
+      float lo[8], hi[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        lo[i] = v[i] * rl;
+        hi[i] = v[i] * rh;
+      }
+      code[h] = cvt_e2m1x8(lo);
+      if (!ts.fits || code[h] != cvt_e2m1x8(hi))
+        code[h] = e2m1x8_exact(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7],
+                               static_cast<double>(s) * static_cast<double>(ts.g));
     }
-    code[0] = cvt_e2m1x8(lo);
-    if (!ts.fits || code[0] != cvt_e2m1x8(hi))
-      code[0] = e2m1x8_exact(f[0], f[1], f[2], f[3], f[4], f[5], f[6], f[7],
-                             static_cast<double>(s) * static_cast<double>(ts.g));
     return sb;
   } else {
-    ab = max(ab, __shfl_xor_sync(0xffffffffu, ab, 2));
+    ab = max(ab, __shfl_xor_sync(0xffffffffu, ab, 1));
     // a = m 2^k, 1 <= m < 2; the largest element is 1.75 * 2^8 (e4m3) or 1.5 * 2^2 (e2m1)
     const uint32_t top = FMT == SV_MXFP8 ? 0x600000u : 0x400000u;
     int k = static_cast<int>(ab >> 23) - 127 - (FMT == SV_MXFP8 ? 8 : 2) + ((ab & 0x7fffffu) > top ? 1 : 0);
     k = max(k, -127);
     const bool bad = ab >= kInfBits;
     const float r = pow2f_bits(bad ? 0 : -k);
-    float q[8];
+    float q[16];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = f[i] * r;
+    for (int i = 0; i < 16; ++i) q[i] = f[i] * r;
     if (FMT == SV_MXFP8) {
-      code[0] = bad ? 0u : cvt_e4m3x4(q);
-      code[1] = bad ? 0u : cvt_e4m3x4(q + 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) code[i] = bad ? 0u : cvt_e4m3x4(q + 4 * i);
     } else {
       code[0] = bad ? 0u : cvt_e2m1x8(q);
+      code[1] = bad ? 0u : cvt_e2m1x8(q + 8);
     }
     return bad ? 0xffu : static_cast<uint32_t>(k + 127);
   }
@@ -245,77 +302,102 @@ __device__ __forceinline__ size_t scale_at(size_t row, int blk, int sp) {
 }
 
 // Writes one lane's codes (when `live`: it holds real columns) and, when `in` (it holds a place of the scale
-// tiles), its block's scale byte, four blocks of a row to a 32-bit store: the padded octets of a row
+// tiles), its block's scale byte, four blocks of a row to a 32-bit store: the padded groups of a row
 // are a whole number of four-block words, so the lanes that hold a word's blocks belong to one row.
 // Every lane of the warp calls it.
 template <int FMT>
-__device__ __forceinline__ void put8(uint8_t* codes, uint8_t* scales, size_t row, int oct, int cols, int sp, bool in,
-                                     bool live, const uint32_t (&code)[2], uint32_t sb) {
-  constexpr int kPer = FMT == SV_NVFP4 ? 2 : 4;  // octets per block
-  const int blk = oct / kPer;
+__device__ __forceinline__ void put16(uint8_t* codes, uint8_t* scales, size_t row, int grp, int cols, int sp, bool in,
+                                      bool live, const uint32_t (&code)[4], uint32_t sb) {
+  constexpr int kPer = FMT == SV_NVFP4 ? 1 : 2;  // groups per block
+  const int blk = grp / kPer;
   uint32_t w = live ? sb << (8 * (blk & 3)) : 0u;
   w |= __shfl_xor_sync(0xffffffffu, w, kPer);
   w |= __shfl_xor_sync(0xffffffffu, w, 2 * kPer);
-  if (in && oct % (4 * kPer) == 0) *reinterpret_cast<uint32_t*>(scales + scale_at(row, blk, sp)) = w;
+  if (in && grp % (4 * kPer) == 0) *reinterpret_cast<uint32_t*>(scales + scale_at(row, blk, sp)) = w;
   if (!live) return;
   if (FMT == SV_MXFP8)
-    *reinterpret_cast<uint2*>(codes + row * cols + static_cast<size_t>(oct) * 8) = make_uint2(code[0], code[1]);
+    *reinterpret_cast<uint4*>(codes + row * cols + static_cast<size_t>(grp) * 16) =
+        make_uint4(code[0], code[1], code[2], code[3]);
   else
-    *reinterpret_cast<uint32_t*>(codes + row * (cols / 2) + static_cast<size_t>(oct) * 4) = code[0];
+    *reinterpret_cast<uint2*>(codes + row * (cols / 2) + static_cast<size_t>(grp) * 8) = make_uint2(code[0], code[1]);
 }
 
-// A block's threads take kUnroll octets each of the (padded row, padded octet) grid, kMxThreads apart: rows
-// rounded up to 128 and op octets per row (a multiple of 16), so every warp is full and the places of the
-// scale tiles that hold no block are written too. step_rows, step_oct: kMxThreads octets in rows and octets.
+// Quotients of n < 2^31 by a divisor known on the host: floor(n m / 2^(31 + s)) with 2^(s - 1) < d <= 2^s and
+// m = floor(2^(31 + s) / d) + 1 (Granlund and Montgomery, 1994).
+struct FastDiv {
+  uint32_t d, m;
+  int s;
+  explicit FastDiv(uint32_t div) : d(div), m(0), s(0) {
+    while ((1ull << s) < d) ++s;
+    m = d > 1 ? static_cast<uint32_t>((1ull << (31 + s)) / d + 1) : 0;
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return d == 1 ? n : __umulhi(n, m) >> (s - 1); }
+};
+
+// Steps through a grid of rows of `per_row` items, kMxThreads items at a time.
 struct Walk {
-  uint32_t row;
-  int oct;
-  __device__ __forceinline__ Walk(size_t idx, uint32_t op)
-      : row(static_cast<uint32_t>(idx / op)), oct(static_cast<int>(idx - static_cast<size_t>(row) * op)) {}
-  __device__ __forceinline__ void next(uint32_t step_rows, int step_oct, int op) {
+  FastDiv per_row;
+  uint32_t step_rows;
+  int step_item;  // kMxThreads in rows and items
+  explicit Walk(int items) : per_row(items), step_rows(kMxThreads / items), step_item(kMxThreads % items) {}
+  __device__ __forceinline__ void start(size_t idx, uint32_t& row, int& item) const {
+    row = idx < 0x80000000ull ? per_row(static_cast<uint32_t>(idx)) : static_cast<uint32_t>(idx / per_row.d);
+    item = static_cast<int>(idx - static_cast<size_t>(row) * per_row.d);
+  }
+  __device__ __forceinline__ void next(uint32_t& row, int& item) const {
     row += step_rows;
-    oct += step_oct;
-    if (oct >= op) oct -= op, ++row;
+    item += step_item;
+    if (item >= static_cast<int>(per_row.d)) item -= per_row.d, ++row;
   }
 };
 
+// A block's threads take kUnroll groups each of the (padded row, padded group) grid, kMxThreads apart: rows
+// rounded up to 128 and gp groups per row (a multiple of 8), so every warp is full and the places of the
+// scale tiles that hold no block are written too.
 template <int FMT, typename T, bool kHeads>
-__global__ void __launch_bounds__(kMxThreads) quantize_kernel(const T* __restrict__ x, int H, int N, int D, uint32_t rows,
-                                                              int cols, int op, int step_rows, int step_oct, int sp,
+__global__ void __launch_bounds__(kMxThreads) quantize_kernel(const T* __restrict__ x, int H, FastDiv N, FastDiv D,
+                                                              uint32_t rows, int cols, Walk walk, int sp,
                                                               uint32_t rows_padded, const float* gscale, uint8_t* codes,
                                                               uint8_t* scales) {
+  uint32_t row;
+  int grp;
+  walk.start(static_cast<size_t>(blockIdx.x) * (kMxThreads * kUnroll) + threadIdx.x, row, grp);
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
-  Walk at(static_cast<size_t>(blockIdx.x) * (kMxThreads * kUnroll) + threadIdx.x, static_cast<uint32_t>(op));
-  Oct<T> v[kUnroll];
+  Cols<T, 16> v[kUnroll];
   {
-    Walk w = at;
+    uint32_t r = row;
+    int it = grp;
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int c = w.oct * kOct;
-      size_t from;
-      if (kHeads) {
-        const uint32_t b = w.row / static_cast<uint32_t>(N), n = w.row - b * static_cast<uint32_t>(N);
-        const uint32_t head = static_cast<uint32_t>(c) / static_cast<uint32_t>(D);
-        from = ((static_cast<size_t>(b) * H + head) * N + n) * D + (c - head * D);
-      } else {
-        from = static_cast<size_t>(w.row) * cols + c;
-      }
+      const int c = it * kGroup;
       v[u].zero();
-      if (w.row < rows && c < cols) v[u].load(x + from);
-      w.next(step_rows, step_oct, op);
+      if (r < rows && c < cols) {
+        if (kHeads) {
+          const uint32_t b = N(r), n = r - b * N.d;
+          const T* p = x + (static_cast<size_t>(b) * H * N.d + n) * D.d;
+          const size_t head_pitch = static_cast<size_t>(N.d) * D.d;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // D is a multiple of 8: an octet lies in one head
+            const uint32_t ch = static_cast<uint32_t>(c) + 8 * h, head = D(ch);
+            v[u].o[h].load(p + head * head_pitch + (ch - head * D.d));
+          }
+        } else {
+          v[u].load(x + static_cast<size_t>(r) * cols + c);
+        }
+      }
+      walk.next(r, it);
     }
   }
   const TensorScale ts = tensor_scale(FMT == SV_NVFP4 ? *gscale : 1.f);
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
-    float f[8];
+    float f[16];
     v[u].get(f);
-    uint32_t code[2];
-    const uint32_t sb = quantise8<FMT>(f, ts, code);
-    put8<FMT>(codes, scales, at.row, at.oct, cols, sp, at.row < rows_padded, at.row < rows && at.oct * kOct < cols, code,
-              sb);
-    at.next(step_rows, step_oct, op);
+    uint32_t code[4];
+    const uint32_t sb = quantise16<FMT>(f, amax16(v[u]), ts, code);
+    put16<FMT>(codes, scales, row, grp, cols, sp, row < rows_padded, row < rows && grp * kGroup < cols, code, sb);
+    walk.next(row, grp);
   }
 }
 
@@ -324,12 +406,13 @@ __global__ void __launch_bounds__(kMxThreads) quantize_kernel(const T* __restric
 template <int FMT, typename T>
 __global__ void __launch_bounds__(kMxThreads) dequantize_kernel(const uint8_t* __restrict__ codes,
                                                                 const uint8_t* __restrict__ scales, const float* gscale,
-                                                                int op, int step_rows, int step_oct, int sp, T* y,
-                                                                size_t total) {
+                                                                Walk walk, int sp, T* y, size_t total) {
+  const size_t idx = static_cast<size_t>(blockIdx.x) * (kMxThreads * kUnroll) + threadIdx.x;
+  uint32_t row;
+  int oct;
+  walk.start(idx, row, oct);
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
-  size_t idx = static_cast<size_t>(blockIdx.x) * (kMxThreads * kUnroll) + threadIdx.x;
-  Walk at(idx, static_cast<uint32_t>(op));
   uint2 c[kUnroll];
   uint32_t sb[kUnroll];
 #pragma unroll
@@ -342,9 +425,9 @@ __global__ void __launch_bounds__(kMxThreads) dequantize_kernel(const uint8_t* _
         c[u] = *reinterpret_cast<const uint2*>(codes + i * 8);
       else
         c[u].x = *reinterpret_cast<const uint32_t*>(codes + i * 4);
-      sb[u] = scales[scale_at(at.row, at.oct / (FMT == SV_NVFP4 ? 2 : 4), sp)];
+      sb[u] = scales[scale_at(row, oct / (FMT == SV_NVFP4 ? 2 : 4), sp)];
     }
-    at.next(step_rows, step_oct, op);
+    walk.next(row, oct);
   }
   const float g = FMT == SV_NVFP4 ? *gscale : 1.f;
 #pragma unroll
@@ -401,76 +484,79 @@ __global__ void __launch_bounds__(kMxThreads) global_scale_kernel(const T* __res
 }
 
 // ---- norm ----
-// A team of blockDim.x threads takes one row (blockDim.y rows per block; more than one only with
-// one-warp teams). Thread t holds the octets i * blockDim.x + t, i < O, in registers from the load to the
-// store, so x and the residual are read once; all loads are issued before the first is used (with the
-// unpacked values in registers and loads between their uses the 720p prefill took 292 us, bound by their
-// latency). Squares are summed in fp64: then 1 / sqrt(mean + eps), rounded to fp32, does not depend on how
-// the row is split over threads (but for one case in about 1e8), and quantised outputs, where a last-bit
-// difference can move an element by a whole step, do not either.
+// A team of blockDim.x threads takes one row (blockDim.y rows per block; more than one only with teams of at
+// most a warp: 8, 16 or 32 lanes). Thread t holds the column groups i * blockDim.x + t, i < O, of E columns (8, or 16 where
+// they are quantised) in registers from the load to the store, so x and the residual are read once; all
+// loads are issued before the first is used (with the unpacked values in registers and loads between
+// their uses the 720p prefill took 292 us, bound by their latency). Squares are summed in fp64: then
+// 1 / sqrt(mean + eps), rounded to fp32, does not depend on how the row is split over threads (but for one
+// case in about 1e8), and quantised outputs, where a last-bit difference can move an element by a whole
+// step, do not either.
 constexpr int kPlain = -1;
 constexpr int kMaxTeam = 512;
 
-__device__ __forceinline__ double warp_sum(double v) {
+// the sum over the lanes of a team (or of its warp)
+__device__ __forceinline__ double team_sum(double v, int team) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = 16; o > 0; o >>= 1) {
+    const double w = __shfl_xor_sync(0xffffffffu, v, o);
+    if (o < team) v += w;
+  }
   return v;
 }
 
 template <int FMT, typename T, int O>
-__global__ void __launch_bounds__(O == 1 || O == 8 ? kMaxTeam : 256)
+__global__ void __launch_bounds__(kMaxTeam)
     rmsnorm_kernel(const T* x, const T* res, T* h_out, const float* __restrict__ w, size_t rows, size_t rows_padded,
-                   int cols, int op, int sp, float eps, T* y, const float* gscale, uint8_t* codes, uint8_t* scales) {
+                   int cols, int gp, int sp, float eps, T* y, const float* gscale, uint8_t* codes, uint8_t* scales) {
   __shared__ double part[kMaxTeam / 32];
   griddep_wait();
   if (threadIdx.x == 0 && threadIdx.y == 0) griddep_launch_dependents();
   const size_t row = static_cast<size_t>(blockIdx.x) * blockDim.y + threadIdx.y;
-  if (row >= rows_padded) return;  // whole warps: with blockDim.y == 1 the whole block
   const int team = blockDim.x;
   const bool real = row < rows;
   const size_t base = row * cols;
-  Oct<T> h[O];
-  {
-    Oct<T> r[O];
+  constexpr int E = FMT == kPlain ? kOct : kGroup;
+  Cols<T, E> h[O];
+#pragma unroll
+  for (int i = 0; i < O; ++i) {
+    const int c = (i * team + static_cast<int>(threadIdx.x)) * E;
+    h[i].zero();
+    if (real && c < cols) h[i].load(x + base + c);
+  }
+  if (res != nullptr) {
+    Cols<T, E> r[O];
 #pragma unroll
     for (int i = 0; i < O; ++i) {
-      const int c = (i * team + static_cast<int>(threadIdx.x)) * kOct;
-      h[i].zero();
-      if (real && c < cols) h[i].load(x + base + c);
+      const int c = (i * team + static_cast<int>(threadIdx.x)) * E;
+      r[i].zero();
+      if (real && c < cols) r[i].load(res + base + c);
     }
-    if (res != nullptr) {
 #pragma unroll
-      for (int i = 0; i < O; ++i) {
-        const int c = (i * team + static_cast<int>(threadIdx.x)) * kOct;
-        r[i].zero();
-        if (real && c < cols) r[i].load(res + base + c);
-      }
+    for (int i = 0; i < O; ++i) {
+      float f[E], q[E];
+      h[i].get(f);
+      r[i].get(q);
 #pragma unroll
-      for (int i = 0; i < O; ++i) {
-        float f[8], q[8];
-        h[i].get(f);
-        r[i].get(q);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] += q[j];
-        h[i].set(f);
-      }
+      for (int j = 0; j < E; ++j) f[j] += q[j];
+      h[i].set(f);
     }
   }
   double s0 = 0.0, s1 = 0.0;
 #pragma unroll
   for (int i = 0; i < O; ++i) {
-    float f[8];
+    float f[E];
     h[i].get(f);
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
+    for (int j = 0; j < E; j += 2) {
       const double a = f[j], b = f[j + 1];
       s0 = fma(a, a, s0);
       s1 = fma(b, b, s1);
     }
-    const int c = (i * team + static_cast<int>(threadIdx.x)) * kOct;
+    const int c = (i * team + static_cast<int>(threadIdx.x)) * E;
     if (h_out != nullptr && real && c < cols) h[i].store(h_out + base + c);
   }
-  double sum = warp_sum(s0 + s1);
+  double sum = team_sum(s0 + s1, team);
   if (team > 32) {
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = sum;
     __syncthreads();
@@ -481,28 +567,31 @@ __global__ void __launch_bounds__(O == 1 || O == 8 ? kMaxTeam : 256)
   const TensorScale ts = tensor_scale(FMT == SV_NVFP4 ? *gscale : 1.f);
 #pragma unroll
   for (int i = 0; i < O; ++i) {
-    const int oct = i * team + static_cast<int>(threadIdx.x);
-    const int c = oct * kOct;
+    const int grp = i * team + static_cast<int>(threadIdx.x);
+    const int c = grp * E;
     const bool live = real && c < cols;
-    float f[8];
+    float f[E];
     h[i].get(f);
     if (live) {
-      const float4 w0 = __ldg(reinterpret_cast<const float4*>(w + c)), w1 = __ldg(reinterpret_cast<const float4*>(w + c) + 1);
-      const float ww[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = f[j] * rstd * ww[j];
+      for (int j = 0; j < E; j += 4) {
+        const float4 ww = __ldg(reinterpret_cast<const float4*>(w + c + j));
+        f[j] = f[j] * rstd * ww.x;
+        f[j + 1] = f[j + 1] * rstd * ww.y;
+        f[j + 2] = f[j + 2] * rstd * ww.z;
+        f[j + 3] = f[j + 3] * rstd * ww.w;
+      }
     }
-    if (FMT == kPlain) {
+    if constexpr (FMT == kPlain) {
       if (live) {
-        Oct<T> o;
+        Cols<T, E> o;
         o.set(f);
         o.store(y + base + c);
       }
     } else {
-      constexpr int F = FMT == kPlain ? 0 : FMT;
-      uint32_t code[2];
-      const uint32_t sb = quantise8<F>(f, ts, code);
-      put8<F>(codes, scales, row, oct, cols, sp, oct < op, live, code, sb);  // the team may cover more than op octets
+      uint32_t code[4];
+      const uint32_t sb = quantise16<FMT>(f, amax16(f), ts, code);
+      put16<FMT>(codes, scales, row, grp, cols, sp, grp < gp && row < rows_padded, live, code, sb);  // the team may cover more than gp groups
     }
   }
 }
@@ -556,15 +645,15 @@ sv_status mx_size(sv_mx_format fmt, long long rows, int cols) {
 template <int FMT, typename T>
 sv_status run_quantize(const void* x, int H, int N, int D, const sv_mx& m, cudaStream_t st) {
   const int sp = mx_padded_blocks(m.fmt, m.cols);
-  const int op = sp * mx_block(m.fmt) / kOct;
+  const int gp = sp * mx_block(m.fmt) / kGroup;
   const long long rows_padded = mx_row_tiles(m.rows) * 128, per = kMxThreads * kUnroll;
-  const long long blocks = (rows_padded * op + per - 1) / per;
+  const long long blocks = (rows_padded * gp + per - 1) / per;
   if (blocks > 0x7fffffffLL) return mfail(SV_ERR_UNSUPPORTED, "too many elements");
   cudaLaunchAttribute at;
   const cudaLaunchConfig_t cfg = pdl_config(dim3(static_cast<unsigned>(blocks)), dim3(kMxThreads), st, &at);
   const auto go = [&](auto kernel) {
-    return launched(cudaLaunchKernelEx(&cfg, kernel, static_cast<const T*>(x), H, N, D, static_cast<uint32_t>(m.rows),
-                                       m.cols, op, kMxThreads / op, kMxThreads % op, sp,
+    return launched(cudaLaunchKernelEx(&cfg, kernel, static_cast<const T*>(x), H, FastDiv(N), FastDiv(D),
+                                       static_cast<uint32_t>(m.rows), m.cols, Walk(gp), sp,
                                        static_cast<uint32_t>(rows_padded), m.gscale, static_cast<uint8_t*>(m.codes),
                                        static_cast<uint8_t*>(m.scales)),
                     "quantisation");
@@ -581,8 +670,8 @@ sv_status run_dequantize(const sv_mx& m, void* y, cudaStream_t st) {
   cudaLaunchAttribute at;
   const cudaLaunchConfig_t cfg = pdl_config(dim3(static_cast<unsigned>(blocks)), dim3(kMxThreads), st, &at);
   return launched(cudaLaunchKernelEx(&cfg, dequantize_kernel<FMT, T>, static_cast<const uint8_t*>(m.codes),
-                                     static_cast<const uint8_t*>(m.scales), m.gscale, op, kMxThreads / op,
-                                     kMxThreads % op, mx_padded_blocks(m.fmt, m.cols), static_cast<T*>(y), total),
+                                     static_cast<const uint8_t*>(m.scales), m.gscale, Walk(op),
+                                     mx_padded_blocks(m.fmt, m.cols), static_cast<T*>(y), total),
                   "dequantisation");
 }
 
@@ -598,8 +687,8 @@ struct NormArgs {
 };
 
 template <int FMT, typename T, int O>
-sv_status launch_norm(const NormArgs& a, int team, int op, int sp, cudaStream_t st) {
-  const int per_block = team == 32 ? 8 : 1;
+sv_status launch_norm(const NormArgs& a, int team, int gp, int sp, cudaStream_t st) {
+  const int per_block = team <= 32 ? 256 / team : 1;
   const long long rows_padded = a.q != nullptr ? mx_row_tiles(a.rows) * 128 : a.rows;
   const long long blocks = (rows_padded + per_block - 1) / per_block;
   cudaLaunchAttribute at;
@@ -607,7 +696,7 @@ sv_status launch_norm(const NormArgs& a, int team, int op, int sp, cudaStream_t 
   return launched(
       cudaLaunchKernelEx(&cfg, rmsnorm_kernel<FMT, T, O>, static_cast<const T*>(a.x), static_cast<const T*>(a.res),
                          static_cast<T*>(a.h), a.w, static_cast<size_t>(a.rows), static_cast<size_t>(rows_padded), a.C,
-                         op, sp, a.eps, static_cast<T*>(a.y), a.q != nullptr ? a.q->gscale : nullptr,
+                         gp, sp, a.eps, static_cast<T*>(a.y), a.q != nullptr ? a.q->gscale : nullptr,
                          a.q != nullptr ? static_cast<uint8_t*>(a.q->codes) : nullptr,
                          a.q != nullptr ? static_cast<uint8_t*>(a.q->scales) : nullptr),
       "norm");
@@ -616,14 +705,15 @@ sv_status launch_norm(const NormArgs& a, int team, int op, int sp, cudaStream_t 
 template <int FMT, typename T>
 sv_status run_norm(const NormArgs& a, int sms, cudaStream_t st) {
   const int sp = a.q != nullptr ? mx_padded_blocks(a.q->fmt, a.C) : 0;
-  const int op = a.q != nullptr ? sp * mx_block(a.q->fmt) / kOct : (a.C + kOct - 1) / kOct;
-  // Few rows: a thread per octet, so that a row's latency is one load's and a short sum's. Many: one warp
-  // to a row while its octets fit ten to a lane, a block of eight octets per thread beyond that.
-  if (a.rows <= 4 * sms && op <= kMaxTeam) return launch_norm<FMT, T, 1>(a, (op + 31) / 32 * 32, op, sp, st);
-  if (op <= 64) return launch_norm<FMT, T, 2>(a, 32, op, sp, st);
-  if (op <= 160) return launch_norm<FMT, T, 5>(a, 32, op, sp, st);
-  if (op <= 320) return launch_norm<FMT, T, 10>(a, 32, op, sp, st);
-  return launch_norm<FMT, T, 8>(a, ((op + 7) / 8 + 31) / 32 * 32, op, sp, st);
+  const int gp = a.q != nullptr ? sp * mx_block(a.q->fmt) / kGroup : (a.C + kOct - 1) / kOct;
+  // Narrow rows: 8, 16 or 32 lanes each. Few rows: a thread per group of columns, so that a row's latency
+  // is one load's and a short sum's. Many: two groups per thread (measured on 55200 x 2560 bf16, plain:
+  // 2 groups 164 us, 1 group 215, a warp per row with 10 groups 167; to SV_MXFP8: 166, 180, 348).
+  constexpr int kWide = FMT == kPlain ? 8 : 4;
+  if (gp <= 32) return launch_norm<FMT, T, 1>(a, gp <= 8 ? 8 : gp <= 16 ? 16 : 32, gp, sp, st);
+  if (a.rows <= 4 * sms && gp <= kMaxTeam) return launch_norm<FMT, T, 1>(a, (gp + 31) / 32 * 32, gp, sp, st);
+  if (gp <= 2 * kMaxTeam) return launch_norm<FMT, T, 2>(a, ((gp + 1) / 2 + 31) / 32 * 32, gp, sp, st);
+  return launch_norm<FMT, T, kWide>(a, ((gp + kWide - 1) / kWide + 31) / 32 * 32, gp, sp, st);
 }
 
 // Calls f<FMT, T>(args...) for a runtime format and type.
