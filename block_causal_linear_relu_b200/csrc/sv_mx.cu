@@ -9,7 +9,7 @@
 // a power of two and the product x * 2^-k is exact, so the conversion instruction rounds correctly.
 // For SV_NVFP4 the fp32 quotients q (of an element, x * fp32(1 / fp32(s g)), and of the scale, a * fp32(1 /
 // fp32(6 g))) are off by at most about 2^-22 relative; when q (1 - 2^-20) and q (1 + 2^-20) convert to the
-// same code no border lies between them and that code is the answer. Otherwise (bf16 inputs and a
+// same code no border lies between them and it is the answer. Otherwise (bf16 inputs and a
 // measured g do lie on borders) it is found exactly: |x| is compared with the borders t * s * g, products
 // of 3 + 4 + 24 bits, in fp64; the scale's quotient a / (6 g) is taken in fp64 (its distance from a border
 // of e4m3 is at least 2^-33 relative, unless it lies on it) and goes to fp32 towards zero with the lost
@@ -32,7 +32,8 @@ namespace {
 constexpr int kOct = 8;           // columns per lane and step: 16 bytes of bf16 (norm and values)
 constexpr int kGroup = 16;        // columns per lane and step where they are quantised
 constexpr int kMxThreads = 256;  // threads of the quantising and dequantising kernels
-constexpr int kUnroll = 2;       // steps per thread there, all loaded before the first is used
+constexpr int kUnroll = 2;       // steps per thread of the first, all loaded before one is used,
+constexpr int kValueUnroll = 4;  // and of the second
 
 // ---- eight columns as loaded (16-byte aligned) ----
 template <typename T>
@@ -234,8 +235,8 @@ __device__ __forceinline__ uint32_t amax16(const Cols<float, 16>& v) {
 
 // One lane's 16 columns, whose largest magnitude has the bits amax, to codes (SV_MXFP8: four words, else
 // two) and the block's scale byte: a block of SV_NVFP4, or half a block of the MX formats, whose lanes 2i
-// and 2i + 1 both have it. Every lane of the warp calls it.
-template <int FMT>
+// and 2i + 1 both have it. kBf16: the values are bf16 numbers. Every lane of the warp calls it.
+template <int FMT, bool kBf16>
 __device__ __forceinline__ uint32_t quantise16(const float (&f)[16], uint32_t amax, const TensorScale& ts,
                                                uint32_t (&code)[4]) {
   uint32_t ab = amax;
@@ -255,22 +256,39 @@ __device__ __forceinline__ uint32_t quantise16(const float (&f)[16], uint32_t am
       code[0] = code[1] = 0u;
       return sb;
     }
+    const float d = s * ts.g;
     float r;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(s * ts.g));  // off by 2^-23 at most
-    const float rl = r * (1.0f - 0x1p-20f), rh = r * (1.0f + 0x1p-20f);
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(d));  // off by 2^-23 at most
+    // A bf16 value lies near a border t * d only if t * d is near a bf16 number, for t = 1, 3, 5 or 7 (the
+    // borders' odd factors): four tests per block in place of a second conversion per element.
+    bool near = true;
+    if (kBf16) {
+      near = !ts.fits;
+#pragma unroll
+      for (int t = 1; t < 8; t += 2) near |= ((__float_as_uint(d * t) + 5u) & 0xffffu) <= 10u;
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const float* v = f + 8 * h;
-      float lo[8], hi[8];
+      if (kBf16) {
+        float q[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        lo[i] = v[i] * rl;
-        hi[i] = v[i] * rh;
+        for (int i = 0; i < 8; ++i) q[i] = v[i] * r;
+        code[h] = cvt_e2m1x8(q);
       }
-      code[h] = cvt_e2m1x8(lo);
-      if (!ts.fits || code[h] != cvt_e2m1x8(hi))
-        code[h] = e2m1x8_exact(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7],
-                               static_cast<double>(s) * static_cast<double>(ts.g));
+      if (near) {
+        const float rl = r * (1.0f - 0x1p-20f), rh = r * (1.0f + 0x1p-20f);
+        float lo[8], hi[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          lo[i] = v[i] * rl;
+          hi[i] = v[i] * rh;
+        }
+        code[h] = cvt_e2m1x8(lo);
+        if (!ts.fits || code[h] != cvt_e2m1x8(hi))
+          code[h] = e2m1x8_exact(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7],
+                                 static_cast<double>(s) * static_cast<double>(ts.g));
+      }
     }
     return sb;
   } else {
@@ -303,8 +321,9 @@ __device__ __forceinline__ size_t scale_at(size_t row, int blk, int sp) {
 
 // Writes one lane's codes (when `live`: it holds real columns) and, when `in` (it holds a place of the scale
 // tiles), its block's scale byte, four blocks of a row to a 32-bit store: the padded groups of a row
-// are a whole number of four-block words, so the lanes that hold a word's blocks belong to one row.
-// Every lane of the warp calls it.
+// are a whole number of four-block words, so the lanes that hold a word's blocks belong to one row (a
+// byte store per block instead of the two shuffles: 5000 x 16384 norm to SV_NVFP4 115 -> 153 us). Every
+// lane of the warp calls it.
 template <int FMT>
 __device__ __forceinline__ void put16(uint8_t* codes, uint8_t* scales, size_t row, int grp, int cols, int sp, bool in,
                                       bool live, const uint32_t (&code)[4], uint32_t sb) {
@@ -395,28 +414,28 @@ __global__ void __launch_bounds__(kMxThreads) quantize_kernel(const T* __restric
     float f[16];
     v[u].get(f);
     uint32_t code[4];
-    const uint32_t sb = quantise16<FMT>(f, amax16(v[u]), ts, code);
+    const uint32_t sb = quantise16<FMT, sizeof(T) == 2>(f, amax16(v[u]), ts, code);
     put16<FMT>(codes, scales, row, grp, cols, sp, row < rows_padded, row < rows && grp * kGroup < cols, code, sb);
     walk.next(row, grp);
   }
 }
 
-// value = element * scale (exact in fp32) * g, rounded once to T; kUnroll octets of the (row, octet) grid
+// value = element * scale (exact in fp32) * g, rounded once to T; kValueUnroll octets of the (row, octet) grid
 // per thread.
 template <int FMT, typename T>
 __global__ void __launch_bounds__(kMxThreads) dequantize_kernel(const uint8_t* __restrict__ codes,
                                                                 const uint8_t* __restrict__ scales, const float* gscale,
                                                                 Walk walk, int sp, T* y, size_t total) {
-  const size_t idx = static_cast<size_t>(blockIdx.x) * (kMxThreads * kUnroll) + threadIdx.x;
+  const size_t idx = static_cast<size_t>(blockIdx.x) * (kMxThreads * kValueUnroll) + threadIdx.x;
   uint32_t row;
   int oct;
   walk.start(idx, row, oct);
   griddep_wait();
   if (threadIdx.x == 0) griddep_launch_dependents();
-  uint2 c[kUnroll];
-  uint32_t sb[kUnroll];
+  uint2 c[kValueUnroll];
+  uint32_t sb[kValueUnroll];
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
+  for (int u = 0; u < kValueUnroll; ++u) {
     const size_t i = idx + static_cast<size_t>(u) * kMxThreads;
     c[u] = make_uint2(0, 0);
     sb[u] = 0;
@@ -431,7 +450,7 @@ __global__ void __launch_bounds__(kMxThreads) dequantize_kernel(const uint8_t* _
   }
   const float g = FMT == SV_NVFP4 ? *gscale : 1.f;
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
+  for (int u = 0; u < kValueUnroll; ++u) {
     const size_t i = idx + static_cast<size_t>(u) * kMxThreads;
     if (i >= total) break;
     float f[8];
@@ -454,32 +473,47 @@ __global__ void __launch_bounds__(kMxThreads) dequantize_kernel(const uint8_t* _
 
 // *g = max over the grid of max |x_i| / 2688. The quotient of non-negative values grows with |x|, so
 // the maximum of the blocks' quotients (as integers: the bits of non-negative floats are ordered, NaN
-// above all) is the quotient of the maximum, in any order. *g is zeroed before the launch.
+// above all) is the quotient of the maximum, in any order. *g is zeroed before the launch, but for one block,
+// which stores its result. Four vectors per thread and step: with one, too few bytes were in flight (bf16
+// 104 MB: 4.6 TB/s).
+constexpr int kMaxBlock = 512;
 template <typename T>
-__global__ void __launch_bounds__(kMxThreads) global_scale_kernel(const T* __restrict__ x, size_t n, float* g) {
+__global__ void __launch_bounds__(kMaxBlock) global_scale_kernel(const T* __restrict__ x, size_t n, float* g) {
   uint32_t a = 0;
-  const size_t step = static_cast<size_t>(gridDim.x) * kMxThreads * 8;
-  for (size_t i = (static_cast<size_t>(blockIdx.x) * kMxThreads + threadIdx.x) * 8; i < n; i += step) {
+  const size_t stride = static_cast<size_t>(gridDim.x) * kMaxBlock * kOct;
+  size_t i = (static_cast<size_t>(blockIdx.x) * kMaxBlock + threadIdx.x) * kOct;
+  const auto take = [&](const Oct<T>& v) {
     float f[8];
-    if (i + 8 <= n) {
-      Oct<T> v;
-      v.load(x + i);
-      v.get(f);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = i + j < n ? static_cast<float>(x[i + j]) : 0.f;
-    }
+    v.get(f);
 #pragma unroll
     for (int j = 0; j < 8; ++j) a = max(a, __float_as_uint(f[j]) & 0x7fffffffu);
+  };
+  for (; i + 3 * stride + kOct <= n; i += 4 * stride) {
+    Oct<T> v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u].load(x + i + u * stride);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) take(v[u]);
   }
+  for (; i + kOct <= n; i += stride) {
+    Oct<T> v;
+    v.load(x + i);
+    take(v);
+  }
+  for (size_t j = i; j < n && j < i + kOct; ++j) a = max(a, __float_as_uint(static_cast<float>(x[j])) & 0x7fffffffu);
   a = __reduce_max_sync(0xffffffffu, a);
-  __shared__ uint32_t part[kMxThreads / 32];
+  __shared__ uint32_t part[kMaxBlock / 32];
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = a;
   __syncthreads();
-  if (threadIdx.x == 0) {
-#pragma unroll
-    for (int w = 1; w < kMxThreads / 32; ++w) a = max(a, part[w]);
-    atomicMax(reinterpret_cast<unsigned int*>(g), __float_as_uint(__uint_as_float(a) / 2688.0f) & 0x7fffffffu);
+  if (threadIdx.x < 32) {
+    a = __reduce_max_sync(0xffffffffu, threadIdx.x < kMaxBlock / 32 ? part[threadIdx.x] : 0u);
+    const uint32_t q = __float_as_uint(__uint_as_float(a) / 2688.0f) & 0x7fffffffu;
+    if (threadIdx.x == 0) {
+      if (gridDim.x == 1)
+        *g = __uint_as_float(q);
+      else
+        atomicMax(reinterpret_cast<unsigned int*>(g), q);
+    }
   }
 }
 
@@ -590,7 +624,7 @@ __global__ void __launch_bounds__(kMaxTeam)
       }
     } else {
       uint32_t code[4];
-      const uint32_t sb = quantise16<FMT>(f, amax16(f), ts, code);
+      const uint32_t sb = quantise16<FMT, false>(f, amax16(f), ts, code);
       put16<FMT>(codes, scales, row, grp, cols, sp, grp < gp && row < rows_padded, live, code, sb);  // the team may cover more than gp groups
     }
   }
@@ -664,7 +698,7 @@ sv_status run_quantize(const void* x, int H, int N, int D, const sv_mx& m, cudaS
 template <int FMT, typename T>
 sv_status run_dequantize(const sv_mx& m, void* y, cudaStream_t st) {
   const int op = m.cols / kOct;
-  const size_t total = static_cast<size_t>(m.rows) * op, per = kMxThreads * kUnroll;
+  const size_t total = static_cast<size_t>(m.rows) * op, per = kMxThreads * kValueUnroll;
   const size_t blocks = (total + per - 1) / per;
   if (blocks > 0x7fffffffull) return mfail(SV_ERR_UNSUPPORTED, "too many elements");
   cudaLaunchAttribute at;
@@ -792,15 +826,18 @@ extern "C" sv_status sv_mx_global_scale(const void* x, long long n, sv_dtype dt,
   int sms = 0;
   MX_TRY(mx_device(&sms));
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaMemsetAsync(g, 0, sizeof(float), st);
-  if (e != cudaSuccess) return launched(e, "tensor scale");
-  const long long per = static_cast<long long>(kMxThreads) * 8;
-  const long long want = (n + per - 1) / per;
-  const unsigned blocks = static_cast<unsigned>(want < 8ll * sms ? want : 8ll * sms);
+  // one block while its eight rounds of four vectors are about the cost of the second launch
+  const long long per = static_cast<long long>(kMaxBlock) * kOct * 4;
+  const long long want = n <= 8 * per ? 1 : (n + per - 1) / per;
+  const unsigned blocks = static_cast<unsigned>(want < 4ll * sms ? want : 4ll * sms);
+  if (blocks > 1) {
+    const cudaError_t e = cudaMemsetAsync(g, 0, sizeof(float), st);
+    if (e != cudaSuccess) return launched(e, "tensor scale");
+  }
   if (dt == SV_BF16)
-    global_scale_kernel<<<blocks, kMxThreads, 0, st>>>(static_cast<const __nv_bfloat16*>(x), static_cast<size_t>(n), g);
+    global_scale_kernel<<<blocks, kMaxBlock, 0, st>>>(static_cast<const __nv_bfloat16*>(x), static_cast<size_t>(n), g);
   else
-    global_scale_kernel<<<blocks, kMxThreads, 0, st>>>(static_cast<const float*>(x), static_cast<size_t>(n), g);
+    global_scale_kernel<<<blocks, kMaxBlock, 0, st>>>(static_cast<const float*>(x), static_cast<size_t>(n), g);
   return launched(cudaGetLastError(), "tensor scale");
 }
 
