@@ -22,7 +22,6 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
-#include <algorithm>
 #include <cstdio>
 #include <mutex>
 
@@ -36,6 +35,7 @@ namespace {
 constexpr int kRows = 128;          // rows of A per CTA
 constexpr int kEpiWarps = 8;        // two per 32-lane quarter of TMEM, which share its column chunks
 constexpr int kThreads = 64 + 32 * kEpiWarps;  // warp 0 copies, warp 1 MMAs, then the epilogue
+constexpr int kPace = 14;           // sixteenths of the next tile's time that a tile's stores are spread over
 constexpr int kStaging = 32 * 128;  // per epilogue warp: 32 rows x 64 bf16
 
 template <int FMT, int CTAS, int NT>
@@ -59,6 +59,8 @@ struct Cfg {
   static constexpr int kAccs = 2 * NT + 2 * kScaleCols <= 512 ? 2 : 1;
   static constexpr uint32_t kScaleCol = kAccs * NT;
   static_assert(kScaleCol + 2 * kScaleCols <= 512, "TMEM columns");
+  // cycles that a run of K takes: 2 per column on the tensor cores, or its bytes at about 60 per cycle
+  static constexpr int kRunCycles = 2 * NT > kStageBytes / 60 ? 2 * NT : kStageBytes / 60;
   static constexpr MxKind kKind = FMT == SV_MXFP8 ? kMx8 : FMT == SV_MXFP4 ? kMx4 : kNv4;
 };
 
@@ -199,7 +201,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t d = tmem + static_cast<uint32_t>(a * NT);
         const int n0 = (tile % g.nt) * NT;
         const uint32_t shift = static_cast<uint32_t>(n0 % 128) / 32;  // columns of B's first scale block before the tile
-        if (!warp_all(mbar_wait(&acce[a], ((tl / C::kAccs) & 1) ^ 1, status, 0x6300u | a))) break;
         for (int kc = 0; kc < g.runs; ++kc) {
           if (!warp_all(mbar_wait(&full[s], phase, status, 0x6310u | s))) {
             ok = false;
@@ -222,6 +223,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int j = 0; j < C::kBBlocks; ++j)
                 tmem_copy_scales<CTAS>(tb + 4 * (t * C::kBBlocks + j), ds + ((1 + j) * C::kScaleBytes >> 4) + 32 * t);
             }
+          }
+          // the accumulator's last tile is drained: asked for after the first run's scales are on their way
+          if (kc == 0) {
+            if (!warp_all(mbar_wait(&acce[a], ((tl / C::kAccs) & 1) ^ 1, status, 0x6300u | a))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+          }
+          if (issue) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
               // step kk (32 bytes on): scale tile t, byte id of its 32-bit cells
@@ -262,6 +273,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int m = tile / g.nt, n0 = (tile - m * g.nt) * NT;
       const int row0 = (m * CTAS + rank) * kRows + q * 32;
       const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(a * NT);
+      // Stores in one burst per tile hold up the loads of the next tile's runs (a run's load took up to 3300
+      // cycles instead of 1000): the warps' chunks go out one by one over the next tile's MMAs, but for the
+      // last tile. Paced so, the 720p Q/K/V projection to nvfp4 went from 546 to 512 us.
+      const long long t0 = clock64();
+      const int gap = CTAS == 2 && tile + step < g.tiles ? g.runs * C::kRunCycles / (kEpiWarps * kRounds) * kPace / 16 : 0;
       const int b0 = kQKV ? row0 / g.N : 0, tok0 = kQKV ? row0 - b0 * g.N : row0;
       // one bulk store takes the warp's 32 rows, unless they run into the next batch
       const bool bulk = CTAS == 2 && (!kQKV || tok0 + 32 <= g.N);
@@ -309,6 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0 && row0 < g.rows) {
+            while (clock64() - t0 < gap * (round * kEpiWarps + warp - 2)) __nanosleep(40);
             tma_store_4d(&maps.o[t], stg, d0, tok0, h, b0);
             bulk_commit();
           }
@@ -435,14 +452,14 @@ sv_status run(const sv_mx& x, const sv_mx& w, const Ops& op, Geo g, void* ws, in
 template <int FMT, bool kQKV>
 sv_status choose(const sv_mx& x, const sv_mx& w, const Ops& op, const Geo& g, void* ws, int sms, cudaStream_t st) {
   if (x.rows <= 128) return run<FMT, 1, 64, kQKV>(x, w, op, g, ws, sms, st);
-  // The column tile with the least cycles: waves of tiles, a run of K taking 2 cycles per column on the
-  // tensor cores or its bytes at about 68 per cycle into an SM, whichever is more.
-  const auto cost = [&](int nt, int bytes) {
+  // the column tile with the least estimated cycles: waves of tiles, each its runs and the draining of the
+  // accumulator
+  const auto cost = [&](int nt, int run_cycles) {
     const long long tiles = (x.rows + 255) / 256 * ((w.rows + nt - 1) / nt);
-    return (tiles + sms / 2 - 1) / (sms / 2) * (static_cast<long long>(g.runs) * std::max(2 * nt, bytes / 68) + 700);
+    return (tiles + sms / 2 - 1) / (sms / 2) * (static_cast<long long>(g.runs) * run_cycles + 700);
   };
-  const long long c128 = cost(128, Cfg<FMT, 2, 128>::kStageBytes), c192 = cost(192, Cfg<FMT, 2, 192>::kStageBytes),
-                  c256 = cost(256, Cfg<FMT, 2, 256>::kStageBytes);
+  const long long c128 = cost(128, Cfg<FMT, 2, 128>::kRunCycles), c192 = cost(192, Cfg<FMT, 2, 192>::kRunCycles),
+                  c256 = cost(256, Cfg<FMT, 2, 256>::kRunCycles);
   if (c256 <= c192 && c256 <= c128) return run<FMT, 2, 256, kQKV>(x, w, op, g, ws, sms, st);
   if (c128 < c192) return run<FMT, 2, 128, kQKV>(x, w, op, g, ws, sms, st);
   return run<FMT, 2, 192, kQKV>(x, w, op, g, ws, sms, st);
