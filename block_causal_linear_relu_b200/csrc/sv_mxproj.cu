@@ -69,6 +69,7 @@ struct Geo {
   int nout;     // output features
   int runs;     // 128-byte runs of K
   int nt;       // column tiles
+  int a_bytes;  // bytes of a run of A that a CTA loads (single CTAs: only the rows there are, rounded up to 8)
   int tiles;    // all tiles
   int N, H, D;  // Q/K/V only: tokens per batch, heads, head features
 };
@@ -163,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t* sc = sb + C::kBBytes;
         if (issue) {
           if (CTAS == 1) {
-            mbar_expect_tx(&full[s], C::kStageBytes);
+            mbar_expect_tx(&full[s], C::kStageBytes - C::kABytes + g.a_bytes);
             tma_load_2d(sa, &maps.a, &full[s], kc * 128, ma * kRows, pol_a);
             tma_load_2d(sb, &maps.b, &full[s], kc * 128, n0, pol_b);
             tma_load_2d(sc, &maps.sa, &full[s], 0, ta, pol_a);
@@ -193,28 +194,36 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {  // scales and MMAs
     if (rank == 0) {
       const bool issue = elect_one();
+      // Per run the loop waits, builds descriptors and issues up to 17 instructions; kept short, it runs
+      // ahead of the MMAs. So each run asks for the next one's data before it issues its own, and the
+      // descriptors of a stage are the first one's low words plus the stage's offset.
+      const uint32_t a0 = smem_u32(smem) >> 4;
+      const uint64_t hi = sdesc_sw128(0, 16, 1024), hi_sc = sdesc_scales(0);
       int s = 0, tl = 0;
-      uint32_t phase = 0, buf = 0;
-      bool ok = true;
+      uint32_t phase = 0, buf = 0, off = 0;
+      bool ok = true, ready = mbar_test(&full[0], 0);
       for (int tile = first; tile < g.tiles && ok; tile += step, ++tl) {
         const int a = tl % C::kAccs;
         const uint32_t d = tmem + static_cast<uint32_t>(a * NT);
         const int n0 = (tile % g.nt) * NT;
         const uint32_t shift = static_cast<uint32_t>(n0 % 128) / 32;  // columns of B's first scale block before the tile
         for (int kc = 0; kc < g.runs; ++kc) {
-          if (!warp_all(mbar_wait(&full[s], phase, status, 0x6310u | s))) {
+          if (!warp_all(ready) && !warp_all(mbar_wait(&full[s], phase, status, 0x6310u | s))) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + s * C::kStride);
-          const uint32_t sb = sa + C::kABytes;
-          const uint32_t sc = sb + C::kBBytes;
-          const uint64_t da = sdesc_sw128(sa, 16, 1024), db = sdesc_sw128(sb, 16, 1024), ds = sdesc_scales(sc);
+          const uint64_t da = hi | (a0 + off), db = hi | (a0 + off + (C::kABytes >> 4)),
+                         ds = hi_sc | (a0 + off + ((C::kABytes + C::kBBytes) >> 4));
+          uint64_t* const done = &empty[s];
+          off += C::kStride >> 4;
+          if (++s == C::kStages) s = 0, phase ^= 1, off = 0;
+          ready = mbar_test(&full[s], phase);
           // Copies and MMAs of one thread run in order, so a copy into a buffer follows the MMAs that
           // read it; two buffers let it run beside the MMAs of the run before.
           const uint32_t ta = tmem + C::kScaleCol + buf * C::kScaleCols;
           const uint32_t tb = ta + 4 * C::kTiles;
+          buf ^= 1;
           if (issue) {
 #pragma unroll
             for (int t = 0; t < C::kTiles; ++t) {
@@ -243,9 +252,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      tb + 4 * C::kBBlocks * t + shift, (kc | kk) != 0 ? 1u : 0u);
             }
             if (CTAS == 1)
-              mma_commit(&empty[s]);
+              mma_commit(done);
             else
-              mma_commit_pair(&empty[s]);
+              mma_commit_pair(done);
             if (kc == g.runs - 1) {
               if (CTAS == 1)
                 mma_commit(&accf[a]);
@@ -254,8 +263,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           __syncwarp();
-          buf ^= 1;
-          if (++s == C::kStages) s = 0, phase ^= 1;
         }
       }
     }
@@ -408,7 +415,10 @@ sv_status run(const sv_mx& x, const sv_mx& w, const Ops& op, Geo g, void* ws, in
   g.tiles = static_cast<int>(tiles);
   const uint64_t bytes = static_cast<uint64_t>(FMT == SV_MXFP8 ? x.cols : x.cols / 2);
   Maps maps;
-  MXP_TRY(encode_bytes_2d(&maps.a, x.codes, bytes, static_cast<uint64_t>(x.rows), kRows));
+  // the other rows of a short tile keep what is in shared memory: an output row depends on its own row of A
+  const uint32_t a_rows = CTAS == 1 && x.rows < kRows ? static_cast<uint32_t>((x.rows + 7) / 8 * 8) : kRows;
+  g.a_bytes = static_cast<int>(a_rows) * 128;
+  MXP_TRY(encode_bytes_2d(&maps.a, x.codes, bytes, static_cast<uint64_t>(x.rows), a_rows));
   MXP_TRY(encode_bytes_2d(&maps.b, w.codes, bytes, static_cast<uint64_t>(w.rows), NT / CTAS));
   MXP_TRY(encode_scale_tiles(&maps.sa, x.scales, static_cast<uint64_t>(sa), C::kTiles));
   MXP_TRY(encode_scale_tiles(&maps.sb, w.scales, static_cast<uint64_t>(sb), C::kTiles));
