@@ -35,6 +35,7 @@ namespace {
 constexpr int kRows = 128;          // rows of A per CTA
 constexpr int kEpiWarps = 8;        // two per 32-lane quarter of TMEM, which share its column chunks
 constexpr int kThreads = 64 + 32 * kEpiWarps;  // warp 0 copies, warp 1 MMAs, then the epilogue
+constexpr int kMaxSplit = 8;        // CTAs that share a tile's K: a portable cluster
 constexpr int kPace = 14;           // sixteenths of the next tile's time that a tile's stores are spread over
 constexpr int kStaging = 32 * 128;  // per epilogue warp: 32 rows x 64 bf16
 
@@ -52,6 +53,7 @@ struct Cfg {
   static constexpr int kStagingOff = kStages * kStride;
   static constexpr int kBarOff = kStagingOff + kEpiWarps * kStaging;
   static constexpr int kSmem = kBarOff + 256 + 1024;  // barriers, TMEM slot, alignment slack
+  static_assert(CTAS == 2 || (NT == 128 && kStagingOff >= kRows * NT * 4), "a tile's fp32 sums fit into the stages");
   static_assert(kSmem <= 227 * 1024 && kStages >= 4, "shared memory of the microscaled product");
   // TMEM columns: the accumulators (two of up to 192 columns; two of 256 and the scales do not fit), then two
   // buffers of scales (A: 4 per tile, B: 4 per tile and block)
@@ -72,6 +74,7 @@ struct Geo {
   int a_bytes;  // bytes of a run of A that a CTA loads (single CTAs: only the rows there are, rounded up to 8)
   int tiles;    // all tiles
   int N, H, D;  // Q/K/V only: tokens per batch, heads, head features
+  int split;    // single CTAs: CTAs of a cluster that share a tile's K
 };
 
 struct Maps {
@@ -84,6 +87,24 @@ struct Ops {
   const float *ga, *gb;         // tensor scales, or NULL
   __nv_bfloat16 *o0, *o1, *o2;  // y, or q, k, v
 };
+
+// Where output feature nc goes: tensor t (0 y or q, 1 k, 2 v), its head and the feature in the head.
+struct Place {
+  int t, h, d;
+};
+template <bool kQKV>
+__device__ __forceinline__ Place place(const Geo& g, int nc) {
+  if (!kQKV) return {0, 0, nc};
+  const int hd = g.H * g.D, t = nc / hd, f = nc - t * hd, h = f / g.D;
+  return {t, h, f - h * g.D};
+}
+template <bool kQKV>
+__device__ __forceinline__ size_t offset(const Geo& g, const Place& p, int row) {
+  if (!kQKV) return static_cast<size_t>(row) * g.nout + p.d;
+  const int b = row / g.N;
+  return ((static_cast<size_t>(b) * g.H + p.h) * g.N + (row - b * g.N)) * g.D + p.d;
+}
+__device__ __forceinline__ __nv_bfloat16* output(const Ops& op, int t) { return t == 0 ? op.o0 : (t == 1 ? op.o1 : op.o2); }
 
 // Tiles are numbered column tile fastest: the CTAs at work share a few row tiles of A (read from DRAM once)
 // and sweep W, which stays in L2. Blocks of 4 or 8 row tiles, which touch fewer distinct tiles at a time,
@@ -105,7 +126,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int rank = CTAS == 2 ? static_cast<int>(cluster_ctarank()) : 0;
-  const int first = static_cast<int>(blockIdx.x) / CTAS, step = static_cast<int>(gridDim.x) / CTAS;
+  const int group = CTAS == 2 ? 2 : g.split;  // CTAs that work on one tile
+  const int first = static_cast<int>(blockIdx.x) / group, step = static_cast<int>(gridDim.x) / group;
+  const int krank = CTAS == 1 && g.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int k0 = CTAS == 2 ? 0 : krank * g.runs / g.split, k1 = CTAS == 2 ? g.runs : (krank + 1) * g.runs / g.split;
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&full[i], 1);
@@ -152,9 +176,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int tile = first; tile < g.tiles && ok; tile += step) {
       const int m = tile / g.nt, n0 = (tile - m * g.nt) * NT;
       const int ma = m * CTAS + rank;  // this CTA's 128 rows
-      int ta = ma * g.runs * C::kTiles;
-      int tb = n0 / 128 * g.runs * C::kTiles;
-      for (int kc = 0; kc < g.runs; ++kc, ta += C::kTiles, tb += C::kTiles) {
+      int ta = (ma * g.runs + k0) * C::kTiles;
+      int tb = (n0 / 128 * g.runs + k0) * C::kTiles;
+      for (int kc = k0; kc < k1; ++kc, ta += C::kTiles, tb += C::kTiles) {
         if (!warp_all(mbar_wait(&empty[s], phase, status, 0x6100u | s))) {
           ok = false;
           break;
@@ -207,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t d = tmem + static_cast<uint32_t>(a * NT);
         const int n0 = (tile % g.nt) * NT;
         const uint32_t shift = static_cast<uint32_t>(n0 % 128) / 32;  // columns of B's first scale block before the tile
-        for (int kc = 0; kc < g.runs; ++kc) {
+        for (int kc = k0; kc < k1; ++kc) {
           if (!warp_all(ready) && !warp_all(mbar_wait(&full[s], phase, status, 0x6310u | s))) {
             ok = false;
             break;
@@ -234,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           // the accumulator's last tile is drained: asked for after the first run's scales are on their way
-          if (kc == 0) {
+          if (kc == k0) {
             if (!warp_all(mbar_wait(&acce[a], ((tl / C::kAccs) & 1) ^ 1, status, 0x6300u | a))) {
               ok = false;
               break;
@@ -249,13 +273,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint32_t id = FMT == SV_NVFP4 ? 0 : FMT == SV_MXFP4 ? (kk & 1) * 2 : kk;
               mma_mx<CTAS, C::kKind>(d, da + 2 * kk, db + 2 * kk,
                                      idesc_mx(kRows * CTAS, NT, FMT == SV_MXFP8 ? 0 : 1, FMT != SV_NVFP4, id), ta + 4 * t,
-                                     tb + 4 * C::kBBlocks * t + shift, (kc | kk) != 0 ? 1u : 0u);
+                                     tb + 4 * C::kBBlocks * t + shift, kc != k0 || kk != 0 ? 1u : 0u);
             }
             if (CTAS == 1)
               mma_commit(done);
             else
               mma_commit_pair(done);
-            if (kc == g.runs - 1) {
+            if (kc == k1 - 1) {
               if (CTAS == 1)
                 mma_commit(&accf[a]);
               else
@@ -284,7 +308,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // cycles instead of 1000): the warps' chunks go out one by one over the next tile's MMAs, but for the
       // last tile. Paced so, the 720p Q/K/V projection to nvfp4 went from 546 to 512 us.
       const long long t0 = clock64();
-      const int gap = CTAS == 2 && tile + step < g.tiles ? g.runs * C::kRunCycles / (kEpiWarps * kRounds) * kPace / 16 : 0;
+      const long long gap = CTAS == 2 && tile + step < g.tiles
+                                ? static_cast<long long>(g.runs) * C::kRunCycles / (kEpiWarps * kRounds) * kPace / 16
+                                : 0;
       const int b0 = kQKV ? row0 / g.N : 0, tok0 = kQKV ? row0 - b0 * g.N : row0;
       // one bulk store takes the warp's 32 rows, unless they run into the next batch
       const bool bulk = CTAS == 2 && (!kQKV || tok0 + 32 <= g.N);
@@ -304,15 +330,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           mbar_arrive_pair(mapa_shared(smem_u32(&acce[a]), 0));
       }
+      if (CTAS == 1 && g.split > 1) {
+        // to this CTA's shared memory, whose stages are free: [128][NT] fp32, a row's 16-byte pieces swizzled by
+        // the row, so that neither these writes (lanes in a column) nor the reads (lanes in a row) collide
+        if (row0 + lane < g.rows) {
+          float4* part = reinterpret_cast<float4*>(smem) + (q * 32 + lane) * (NT / 4);
+#pragma unroll
+          for (int round = 0; round < kRounds; ++round)
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (2 * round + half < kChunks)
+                part[((2 * round + half) * 16 + j) ^ lane] =
+                    make_float4(__uint_as_float(rr[round][4 * j]), __uint_as_float(rr[round][4 * j + 1]),
+                                __uint_as_float(rr[round][4 * j + 2]), __uint_as_float(rr[round][4 * j + 3]));
+        }
+        continue;
+      }
 #pragma unroll
       for (int round = 0; round < kRounds; ++round) {
         const int c = 2 * round + half;  // the quarter's two warps take neighbouring chunks
         const int nc = n0 + c * 64;  // first output feature of the chunk
         if (c >= kChunks || nc >= g.nout) continue;
-        const int hd = kQKV ? g.H * g.D : g.nout;
-        const int t = kQKV ? nc / hd : 0, f = nc - t * hd;  // tensor, feature in it
-        const int h = kQKV ? f / g.D : 0, d0 = kQKV ? f - h * g.D : f;
-        const bool relu = kQKV && t < 2;
+        const Place p = place<kQKV>(g, nc);
+        const bool relu = kQKV && p.t < 2;
         if (CTAS == 2) {  // the last bulk store has read the buffer
           if (lane == 0) bulk_wait_read_all();
           __syncwarp();
@@ -333,22 +373,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0 && row0 < g.rows) {
             while (clock64() - t0 < gap * (round * kEpiWarps + warp - 2)) __nanosleep(40);
-            tma_store_4d(&maps.o[t], stg, d0, tok0, h, b0);
+            tma_store_4d(&maps.o[p.t], stg, p.d, tok0, p.h, b0);
             bulk_commit();
           }
           __syncwarp();
         } else {
           __syncwarp();
-          __nv_bfloat16* out = t == 0 ? op.o0 : (t == 1 ? op.o1 : op.o2);
+          __nv_bfloat16* out = output(op, p.t) + piece * 8;
           const bool col_ok = nc + piece * 8 < g.nout;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int r = 4 * i + sub;
             const uint4 w = *reinterpret_cast<const uint4*>(stg + r * 128 + ((piece ^ (r & 7)) << 4));
-            const int b = kQKV ? (row0 + r) / g.N : 0;
-            const size_t at = kQKV ? ((static_cast<size_t>(b) * g.H + h) * g.N + (row0 + r - b * g.N)) * g.D + d0
-                                   : static_cast<size_t>(row0 + r) * g.nout + d0;
-            if (col_ok && row0 + r < g.rows) *reinterpret_cast<uint4*>(out + at + piece * 8) = w;
+            if (col_ok && row0 + r < g.rows) *reinterpret_cast<uint4*>(out + offset<kQKV>(g, p, row0 + r)) = w;
           }
         }
         __syncwarp();
@@ -358,8 +395,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (CTAS == 2) {  // neither CTA leaves while the other may still signal its barriers or read its operands
+  if (CTAS == 2 || g.split > 1) {  // neither CTA leaves while the other may still signal its barriers or read its operands
     cluster_arrive_release();
+    cluster_wait_acquire();
+  }
+  if (CTAS == 1 && g.split > 1) {  // each CTA adds its share of the tile's (row, four columns) items
+    const int m = first / g.nt, n0 = (first - m * g.nt) * NT;
+    const int rows = min(kRows, g.rows - m * kRows);
+    const float alpha = FMT == SV_NVFP4 ? *op.ga * *op.gb : 1.f;
+    constexpr int kPieces = NT / 4;
+    for (int i = krank * kThreads + static_cast<int>(threadIdx.x); i < rows * kPieces; i += g.split * kThreads) {
+      const int r = i / kPieces, c4 = i - r * kPieces;  // a warp reads whole rows of a rank: 512 bytes
+      const uint32_t at = smem_u32(smem) + static_cast<uint32_t>(r * NT * 4 + ((c4 ^ (r & 31)) << 4));
+      float4 v[kMaxSplit];
+#pragma unroll
+      for (int c = 0; c < kMaxSplit; ++c) {
+        v[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c < g.split) v[c] = ld_shared_cluster_f4(mapa_shared(at, static_cast<uint32_t>(c)));
+      }
+      float f[4] = {};
+#pragma unroll
+      for (int c = 0; c < kMaxSplit; ++c) f[0] += v[c].x, f[1] += v[c].y, f[2] += v[c].z, f[3] += v[c].w;
+      const int nc = n0 + c4 * 4;
+      if (nc >= g.nout) continue;
+      const Place p = place<kQKV>(g, nc);
+      uint2 w = make_uint2(pack_bf16x2(f[0] * alpha, f[1] * alpha), pack_bf16x2(f[2] * alpha, f[3] * alpha));
+      if (kQKV && p.t < 2) w = make_uint2(relu_bf16x2(w.x), relu_bf16x2(w.y));
+      *reinterpret_cast<uint2*>(output(op, p.t) + offset<kQKV>(g, p, m * kRows + r)) = w;
+    }
+    cluster_arrive_release();  // the others may still read this CTA's sums
     cluster_wait_acquire();
   }
   if (warp == 1) {
@@ -383,23 +447,56 @@ sv_status pfail(sv_status st, const char* fmt, long long a = 0, long long b = 0)
     if (_s != SV_OK) return _s;   \
   } while (0)
 
-// The kernel's shared-memory attribute, set once per device (and per kernel), thread-safe.
+// Per device (and kernel), looked up once, thread-safe: sets the shared-memory attribute; for single CTAs
+// also how many clusters of 1 .. 8 of them run at the same time (a cluster lives in one GPC).
+struct DevFacts {
+  bool done;
+  int clusters[kMaxSplit + 1];
+};
+cudaLaunchConfig_t config(unsigned ctas, int cluster, int smem, cudaStream_t st, cudaLaunchAttribute (&at)[2]) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = st;
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cfg;
+}
 template <int FMT, int CTAS, int NT, bool kQKV>
-cudaError_t ensure_attr() {
+cudaError_t device_facts(int sms, DevFacts& out) {
+  using C = Cfg<FMT, CTAS, NT>;
   constexpr int kMaxDev = 64;
   static std::mutex mu;
-  static bool done[kMaxDev] = {};
+  static DevFacts facts[kMaxDev] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= kMaxDev) return cudaErrorInvalidDevice;
   std::lock_guard<std::mutex> lock(mu);
-  if (!done[dev]) {
-    e = cudaFuncSetAttribute(mxproj_kernel<FMT, CTAS, NT, kQKV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             Cfg<FMT, CTAS, NT>::kSmem);
+  DevFacts& f = facts[dev];
+  if (!f.done) {
+    const auto kernel = mxproj_kernel<FMT, CTAS, NT, kQKV>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    done[dev] = true;
+    f.clusters[1] = sms;
+    for (int c = 2; CTAS == 1 && c <= kMaxSplit; ++c) {
+      cudaLaunchAttribute at[2];
+      const cudaLaunchConfig_t cfg = config(static_cast<unsigned>(c), c, C::kSmem, nullptr, at);
+      if (cudaOccupancyMaxActiveClusters(&f.clusters[c], kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        f.clusters[c] = 0;  // not used
+      }
+    }
+    f.done = true;
   }
+  out = f;
   return cudaSuccess;
 }
 
@@ -414,6 +511,7 @@ sv_status run(const sv_mx& x, const sv_mx& w, const Ops& op, Geo g, void* ws, in
     return pfail(SV_ERR_UNSUPPORTED, "too many output tiles or scale tiles");
   g.tiles = static_cast<int>(tiles);
   const uint64_t bytes = static_cast<uint64_t>(FMT == SV_MXFP8 ? x.cols : x.cols / 2);
+  g.split = 1;
   Maps maps;
   // the other rows of a short tile keep what is in shared memory: an output row depends on its own row of A
   const uint32_t a_rows = CTAS == 1 && x.rows < kRows ? static_cast<uint32_t>((x.rows + 7) / 8 * 8) : kRows;
@@ -436,23 +534,23 @@ sv_status run(const sv_mx& x, const sv_mx& w, const Ops& op, Geo g, void* ws, in
       MXP_TRY(encode_bf16_4d(&maps.o[0], op.o0, dims, pitch, box));
     }
   }
-  cudaError_t e = ensure_attr<FMT, CTAS, NT, kQKV>();
+  DevFacts facts;
+  cudaError_t e = device_facts<FMT, CTAS, NT, kQKV>(sms, facts);
   if (e == cudaSuccess) {
-    const int groups = sms / CTAS;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>((g.tiles < groups ? g.tiles : groups) * CTAS));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = C::kSmem;
-    cfg.stream = st;
+    if (CTAS == 1) {  // the split of K with the least estimated cycles: 450 a run; the sums' meeting 1800, and 32 a row
+      const long long meet = 1800 + 32 * (x.rows < kRows ? x.rows : kRows);
+      long long best = 0;
+      for (int c = 1; c <= kMaxSplit && c <= g.runs; ++c) {
+        if (facts.clusters[c] < 1 || (c > 1 && tiles > facts.clusters[c])) continue;
+        const long long waves = (tiles + facts.clusters[c] - 1) / facts.clusters[c];
+        const long long cycles = waves * (450ll * ((g.runs + c - 1) / c) + 1000) + (c > 1 ? meet : 0);
+        if (c == 1 || cycles < best) best = cycles, g.split = c;
+      }
+    }
+    const int group = CTAS == 2 ? 2 : g.split, groups = sms / group;
     cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = CTAS;
-    at[1].val.clusterDim.y = 1;
-    at[1].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = CTAS == 2 ? 2 : 1;
+    const cudaLaunchConfig_t cfg =
+        config(static_cast<unsigned>((g.tiles < groups || g.split > 1 ? g.tiles : groups) * group), group, C::kSmem, st, at);
     e = cudaLaunchKernelEx(&cfg, mxproj_kernel<FMT, CTAS, NT, kQKV>, maps, op, g, static_cast<uint32_t*>(ws));
   }
   if (e != cudaSuccess) return pfail(SV_ERR_CUDA, "microscaled product launch failed (%lld)", static_cast<long long>(e));
@@ -461,7 +559,8 @@ sv_status run(const sv_mx& x, const sv_mx& w, const Ops& op, Geo g, void* ws, in
 
 template <int FMT, bool kQKV>
 sv_status choose(const sv_mx& x, const sv_mx& w, const Ops& op, const Geo& g, void* ws, int sms, cudaStream_t st) {
-  if (x.rows <= 128) return run<FMT, 1, 64, kQKV>(x, w, op, g, ws, sms, st);
+  const long long tiles = mx_row_tiles(x.rows) * ((w.rows + 127) / 128);
+  if (x.rows <= kRows || tiles <= sms / 2) return run<FMT, 1, 128, kQKV>(x, w, op, g, ws, sms, st);
   // the column tile with the least estimated cycles: waves of tiles, each its runs and the draining of the
   // accumulator
   const auto cost = [&](int nt, int run_cycles) {
