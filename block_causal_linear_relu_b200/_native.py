@@ -671,6 +671,8 @@ def _mx_workspace(device, stream):
     so calls on several streams share it."""
     ws = _mx_ws.get(device.index)
     if ws is None:
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("the microscaled products' workspace must exist before a capture: make a call first, or pass ws")
         with torch.cuda.device(device):
             ws = _mx_ws[device.index] = Workspace(256, device, stream)
     ws.check(stream)

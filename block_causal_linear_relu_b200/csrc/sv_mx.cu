@@ -32,10 +32,7 @@ namespace {
 constexpr int kOct = 8;           // columns per lane and step: 16 bytes of bf16 (norm and values)
 constexpr int kGroup = 16;        // columns per lane and step where they are quantised
 constexpr int kMxThreads = 256;  // threads of the quantising and dequantising kernels
-// steps per thread of the first, all loaded before one is used, and of the second (20240 x 2560 bf16 to
-// SV_NVFP4: 34.1 us with two steps, 32.4 with four; to SV_MXFP8 26.0 and 27.5)
-template <int FMT, typename T>
-constexpr int kUnroll = FMT == SV_NVFP4 && sizeof(T) == 2 ? 4 : 2;
+// steps per thread of the second, all loaded before one is used; the first takes two or four (below)
 constexpr int kValueUnroll = 4;
 
 // ---- eight columns as loaded (16-byte aligned) ----
@@ -263,12 +260,14 @@ __device__ __forceinline__ uint32_t quantise16(const float (&f)[16], uint32_t am
     float r;
     asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(d));  // off by 2^-23 at most
     // A bf16 value lies near a border t * d only if t * d is near a bf16 number, for t = 1, 3, 5 or 7 (the
-    // borders' odd factors): four tests per block in place of a second conversion per element.
+    // borders' odd factors): four tests per block in place of a second conversion per element. Near: the
+    // code of q can be wrong only within 2^-22 of a border, and d * t is off by 2^-23, which is 6 of its
+    // last places at most.
     bool near = true;
     if (kBf16) {
       near = !ts.fits;
 #pragma unroll
-      for (int t = 1; t < 8; t += 2) near |= ((__float_as_uint(d * t) + 5u) & 0xffffu) <= 10u;
+      for (int t = 1; t < 8; t += 2) near |= ((__float_as_uint(d * t) + 8u) & 0xffffu) <= 16u;
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -373,15 +372,16 @@ struct Walk {
   }
 };
 
-// A block's threads take kUnroll groups each of the (padded row, padded group) grid, kMxThreads apart: rows
+// A block's threads take kSteps groups each of the (padded row, padded group) grid, kMxThreads apart: rows
 // rounded up to 128 and gp groups per row (a multiple of 8), so every warp is full and the places of the
-// scale tiles that hold no block are written too.
-template <int FMT, typename T, bool kHeads>
-__global__ void __launch_bounds__(kMxThreads) quantize_kernel(const T* __restrict__ x, int H, FastDiv N, FastDiv D,
+// scale tiles that hold no block are written too. Two steps; four, in 64 registers, for bf16 to SV_NVFP4 once
+// they fill the device (20240 x 2560, heads: 30.7 us; two steps 35.1, four in 97 registers 40.2; a block of
+// 2760 rows: 6.7 and 5.7 us). The conversions to e2m1 (8 cycles a pair and warp) bound it there.
+template <int FMT, typename T, bool kHeads, int kSteps>
+__global__ void __launch_bounds__(kMxThreads, kSteps == 4 ? 4 : 1) quantize_kernel(const T* __restrict__ x, int H, FastDiv N, FastDiv D,
                                                               uint32_t rows, int cols, Walk walk, int sp,
                                                               uint32_t rows_padded, const float* gscale, uint8_t* codes,
                                                               uint8_t* scales) {
-  constexpr int kSteps = kUnroll<FMT, T>;
   uint32_t row;
   int grp;
   walk.start(static_cast<size_t>(blockIdx.x) * (kMxThreads * kSteps) + threadIdx.x, row, grp);
@@ -681,22 +681,26 @@ sv_status mx_size(sv_mx_format fmt, long long rows, int cols) {
   } while (0)
 
 template <int FMT, typename T>
-sv_status run_quantize(const void* x, int H, int N, int D, const sv_mx& m, cudaStream_t st) {
+sv_status run_quantize(const void* x, int H, int N, int D, const sv_mx& m, int sms, cudaStream_t st) {
   const int sp = mx_padded_blocks(m.fmt, m.cols);
   const int gp = sp * mx_block(m.fmt) / kGroup;
-  const long long rows_padded = mx_row_tiles(m.rows) * 128, per = kMxThreads * kUnroll<FMT, T>;
-  const long long blocks = (rows_padded * gp + per - 1) / per;
-  if (blocks > 0x7fffffffLL) return mfail(SV_ERR_UNSUPPORTED, "too many elements");
-  cudaLaunchAttribute at;
-  const cudaLaunchConfig_t cfg = pdl_config(dim3(static_cast<unsigned>(blocks)), dim3(kMxThreads), st, &at);
-  const auto go = [&](auto kernel) {
+  const long long rows_padded = mx_row_tiles(m.rows) * 128, groups = rows_padded * gp;
+  if (groups / (2 * kMxThreads) > 0x7ffffffeLL) return mfail(SV_ERR_UNSUPPORTED, "too many elements");
+  const auto go = [&](auto kernel, int steps) {
+    const unsigned blocks = static_cast<unsigned>((groups + kMxThreads * steps - 1) / (kMxThreads * steps));
+    cudaLaunchAttribute at;
+    const cudaLaunchConfig_t cfg = pdl_config(dim3(blocks), dim3(kMxThreads), st, &at);
     return launched(cudaLaunchKernelEx(&cfg, kernel, static_cast<const T*>(x), H, FastDiv(N), FastDiv(D),
                                        static_cast<uint32_t>(m.rows), m.cols, Walk(gp), sp,
                                        static_cast<uint32_t>(rows_padded), m.gscale, static_cast<uint8_t*>(m.codes),
                                        static_cast<uint8_t*>(m.scales)),
                     "quantisation");
   };
-  return H == 1 ? go(quantize_kernel<FMT, T, false>) : go(quantize_kernel<FMT, T, true>);
+  if constexpr (FMT == SV_NVFP4 && sizeof(T) == 2) {
+    if (groups >= 4ll * sms * 4 * kMxThreads)
+      return H == 1 ? go(quantize_kernel<FMT, T, false, 4>, 4) : go(quantize_kernel<FMT, T, true, 4>, 4);
+  }
+  return H == 1 ? go(quantize_kernel<FMT, T, false, 2>, 2) : go(quantize_kernel<FMT, T, true, 2>, 2);
 }
 
 template <int FMT, typename T>
@@ -858,7 +862,7 @@ extern "C" sv_status sv_mx_quantize(const void* x, int B, int H, int N, int D, s
   if (x == nullptr || !aligned(x, 16)) return mfail(SV_ERR_INVALID_ARG, "x must be non-NULL and 16-byte aligned");
   int sms = 0;
   MX_TRY(mx_device(&sms));
-  MX_DISPATCH(out->fmt, dt, run_quantize, x, H, N, D, *out, reinterpret_cast<cudaStream_t>(stream));
+  MX_DISPATCH(out->fmt, dt, run_quantize, x, H, N, D, *out, sms, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" sv_status sv_mx_dequantize(const sv_mx* in, void* y, sv_dtype dt, sv_stream_t stream) {

@@ -131,7 +131,70 @@ def test_nvfp4_borders_of_a_measured_scale(sv):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-@pytest.mark.parametrize("n", [1, 7, 8, 2049, 100003])
+def test_nvfp4_tensor_scales_next_to_nice_numbers(sv, dt):
+    # s * g a few last places from a number whose borders are bf16 values: on, just below and just above ties
+    x = make((24, 256), dt, 50, odd=False)
+    for base in (1.0, 0.0625, 1.0 / 3.0, 5.0 / 7.0, 1.9921875):
+        for k in range(-9, 10):
+            g = torch.tensor([base], dtype=torch.float32).view(torch.int32).add(k).view(torch.float32).cuda()
+            e, s, _ = read(sv.sv_mx_quantize(x, sv.SV_NVFP4, gscale=g), "nvfp4")
+            rc, rs = M.quantize(f64(x), "nvfp4", float(g.item()))
+            assert np.array_equal(s, rs) and same(e, M.elements(rc, "nvfp4")), (base, k)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("heads", [False, True])
+def test_large_inputs_equal_their_slices(sv, fmt, heads):
+    # 11 million values: the kernels chosen for large inputs, against small calls on slices
+    B, H, N, D = (3, 20, 1411, 128) if heads else (1, 1, 4233, 2560)
+    g = scale_for(sv, fmt)
+    x = make((B, H, N, D), "bf16", 51, odd=False)
+    big = sv.sv_mx_quantize(x if heads else x.view(N, D), fid(sv, fmt), gscale=g)
+    values = sv.sv_mx_dequantize(big)
+    R = B * N
+    codes, scales = big.codes, M.untile_scales(big.scales.cpu().numpy(), R, H * D // M.BLOCK[fmt])
+    for b in range(B):
+        for n0 in (0, 640, N - 300):
+            part = x[b:b + 1, :, n0:n0 + 300].contiguous()
+            q = sv.sv_mx_quantize(part if heads else part.view(300, D), fid(sv, fmt), gscale=g)
+            at = slice(b * N + n0, b * N + n0 + 300)
+            assert torch.equal(q.codes, codes[at])
+            assert np.array_equal(M.untile_scales(q.scales.cpu().numpy(), 300, H * D // M.BLOCK[fmt]), scales[at])
+            assert torch.equal(sv.sv_mx_dequantize(q), values[at])
+    pad = big.scales.cpu().numpy().copy()
+    pad[np.arange(R)[:, None] // 128, np.arange(scales.shape[1]) // 4, np.arange(R)[:, None] % 32,
+        np.arange(R)[:, None] // 32 % 4, np.arange(scales.shape[1]) % 4] = 0
+    assert not pad.any()
+
+
+def test_offsets_past_32_bits(sv):
+    # 2.2e9 values: the last rows of one call equal a call on those rows alone
+    R, C, last = 68001, 32768, 257
+    x = torch.empty(R, C, dtype=torch.bfloat16, device="cuda")
+    x[:-last] = 1.0
+    x[-last:] = make((last, C), "bf16", 52, odd=False)
+    tail = x[-last:].clone()
+    q, t = sv.sv_mx_quantize(x, sv.SV_MXFP8), sv.sv_mx_quantize(tail, sv.SV_MXFP8)
+    assert torch.equal(q.codes[-last:], t.codes)
+    v = sv.sv_mx_dequantize(q)
+    assert torch.equal(v[-last:], sv.sv_mx_dequantize(t)) and (v[:3] == 1).all()
+    del v
+    w = make((C,), "f32", 53, odd=False)
+    y, h = sv.sv_rmsnorm(x, w, residual=x)
+    y2, h2 = sv.sv_rmsnorm(tail, w, residual=tail)
+    assert torch.equal(y[-last:], y2) and torch.equal(h[-last:], h2)
+    del y, h, q, x
+    R, C, F = 300001, 32, 8192
+    xq, _ = operand(sv, R, C, "mxfp4", 54)
+    wq, _ = operand(sv, F, C, "mxfp4", 55)
+    y = sv.sv_mx_projection(xq, wq)  # 2.5e9 outputs
+    xv = sv.sv_mx_dequantize(xq, torch.float32)
+    tail = sv.sv_mx_quantize(xv[-257:].contiguous(), sv.SV_MXFP4)  # already representable: the same operand
+    assert torch.equal(y[-257:], sv.sv_mx_projection(tail, wq))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 7, 8, 2049, 100003, 700001])
 def test_global_scale(sv, dt, n):
     x = make((n,), dt, n, odd=False)
     assert float(sv.sv_mx_global_scale(x).item()) == float(np.float32(f64(x.abs().max())) / np.float32(2688))
@@ -143,7 +206,8 @@ def test_global_scale(sv, dt, n):
 
 # ---- norm ----
 
-NORM = [(1, 32), (1, 2560), (3, 8), (130, 104), (257, 2592), (5, 520), (9, 1024), (11, 5120), (7, 16384), (2, 32768)]
+NORM = [(1, 32), (1, 2560), (3, 8), (130, 104), (257, 2592), (5, 520), (9, 1024), (11, 5120), (7, 16384), (2, 32768),
+        (700, 264), (601, 2592), (650, 5120), (600, 8192)]  # many rows: two groups of columns per thread
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
@@ -162,7 +226,8 @@ def test_rmsnorm(sv, dt, res, R, C):
 
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
-@pytest.mark.parametrize("R,C", [(1, 32), (1, 2560), (130, 96), (257, 2592), (5, 544), (9, 1024), (11, 5120), (300, 7680), (3, 32768)])
+@pytest.mark.parametrize("R,C", [(1, 32), (1, 2560), (130, 96), (257, 2592), (5, 544), (9, 1024), (11, 5120), (300, 7680), (3, 32768),
+                                 (700, 544), (601, 2592), (600, 8224)])
 def test_rmsnorm_quantised(sv, fmt, dt, R, C):
     x, r = make((R, C), dt, 4, odd=False), make((R, C), dt, 5, odd=False)
     w = make((C,), "f32", 6, odd=False)
@@ -253,6 +318,26 @@ def test_projection_over_many_tiles_per_block(sv, fmt):
     y = sv.sv_mx_projection(xq, wq)
     check_product(y, xv, wv, 640)
     assert torch.equal(y, sv.sv_mx_projection(xq, wq))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("R,C,F", [(18900, 64, 128), (18900, 96, 192), (18900, 64, 256), (18700, 320, 248), (9400, 576, 376)])
+def test_projection_column_tiles(sv, fmt, R, C, F):
+    # one wave of 256-row tiles: each width of the column tile is the best one for some of these
+    xq, xv = operand(sv, R, C, fmt, 70)
+    wq, wv = operand(sv, F, C, fmt, 71, C**-0.5)
+    check_product(sv.sv_mx_projection(xq, wq), xv, wv, C)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("B,N,C,H,D", [(700, 3, 96, 20, 64), (90, 33, 64, 20, 128), (9, 300, 128, 24, 64), (1, 5000, 64, 4, 128)])
+def test_qkv_projection_of_many_short_batches(sv, fmt, B, N, C, H, D):
+    # rows of several batches in the 32 rows of one store
+    xq, xv = operand(sv, B * N, C, fmt, 72)
+    wq, wv = operand(sv, 3 * H * D, C, fmt, 73, C**-0.5)
+    for t, y in enumerate(sv.sv_mx_qkv_projection(xq, wq, B, N, H, D)):
+        rows = y.permute(0, 2, 1, 3).reshape(B * N, H * D)
+        check_product(rows, xv, wv[t * H * D:(t + 1) * H * D], C, relu=t < 2)
 
 
 @pytest.mark.parametrize("fmt", FMTS)
@@ -348,6 +433,31 @@ def test_captured_and_replayed(sv):
         torch.cuda.synchronize()
         for a, b in zip(out, layer()):
             assert torch.equal(a, b)
+
+
+def test_first_call_inside_a_capture_is_refused(sv):
+    from block_causal_linear_relu_b200 import _native
+    xq, _ = operand(sv, 16, 64, "mxfp8", 60)
+    wq, _ = operand(sv, 16, 64, "mxfp8", 61)
+    sv.sv_mx_projection(xq, wq)
+    torch.cuda.synchronize()
+    kept = dict(_native._mx_ws)
+    _native._mx_ws.clear()
+    try:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph), pytest.raises(RuntimeError):
+            sv.sv_mx_projection(xq, wq)
+    finally:
+        _native._mx_ws.update(kept)
+    y = torch.empty(16, 16, dtype=torch.bfloat16, device="cuda")
+    ws = sv.Workspace(256, y.device)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sv.sv_mx_projection(xq, wq, y=y, ws=ws)
+    y.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, sv.sv_mx_projection(xq, wq))
 
 
 def test_two_streams_at_once(sv):
