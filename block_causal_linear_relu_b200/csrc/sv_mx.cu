@@ -378,7 +378,7 @@ struct Walk {
 // they fill the device (20240 x 2560, heads: 30.7 us; two steps 35.1, four in 97 registers 40.2; a block of
 // 2760 rows: 6.7 and 5.7 us). The conversions to e2m1 (8 cycles a pair and warp) bound it there.
 template <int FMT, typename T, bool kHeads, int kSteps>
-__global__ void __launch_bounds__(kMxThreads, kSteps == 4 ? 4 : 1) quantize_kernel(const T* __restrict__ x, int H, FastDiv N, FastDiv D,
+__global__ void __launch_bounds__(kMxThreads, 4) quantize_kernel(const T* __restrict__ x, int H, FastDiv N, FastDiv D,
                                                               uint32_t rows, int cols, Walk walk, int sp,
                                                               uint32_t rows_padded, const float* gscale, uint8_t* codes,
                                                               uint8_t* scales) {
@@ -478,33 +478,42 @@ __global__ void __launch_bounds__(kMxThreads) dequantize_kernel(const uint8_t* _
 // *g = max over the grid of max |x_i| / 2688. The quotient of non-negative values grows with |x|, so
 // the maximum of the blocks' quotients (as integers: the bits of non-negative floats are ordered, NaN
 // above all) is the quotient of the maximum, in any order. *g is zeroed before the launch, but for one block,
-// which stores its result. Four vectors per thread and step: with one, too few bytes were in flight (bf16
-// 104 MB: 4.6 TB/s).
+// which stores its result. Four vectors per thread and step, so that enough bytes are in flight; from the
+// end to the start, so that the quantisation that follows finds the first part of x in L2.
+__global__ void zero_scale_kernel(float* g) {  // instead of a memset: the next launch overlaps with it
+  griddep_launch_dependents();
+  griddep_wait();
+  *g = 0.f;
+}
+
 constexpr int kMaxBlock = 512;
 template <typename T>
 __global__ void __launch_bounds__(kMaxBlock) global_scale_kernel(const T* __restrict__ x, size_t n, float* g) {
+  griddep_wait();
+  if (threadIdx.x == 0) griddep_launch_dependents();
   uint32_t a = 0;
-  const size_t stride = static_cast<size_t>(gridDim.x) * kMaxBlock * kOct;
-  size_t i = (static_cast<size_t>(blockIdx.x) * kMaxBlock + threadIdx.x) * kOct;
+  const size_t vecs = n / kOct, stride = static_cast<size_t>(gridDim.x) * kMaxBlock;
+  size_t i = static_cast<size_t>(blockIdx.x) * kMaxBlock + threadIdx.x;
   const auto take = [&](const Oct<T>& v) {
     float f[8];
     v.get(f);
 #pragma unroll
     for (int j = 0; j < 8; ++j) a = max(a, __float_as_uint(f[j]) & 0x7fffffffu);
   };
-  for (; i + 3 * stride + kOct <= n; i += 4 * stride) {
+  if (i < n % kOct) a = __float_as_uint(static_cast<float>(x[vecs * kOct + i])) & 0x7fffffffu;
+  const T* last = x + (vecs - 1) * kOct;  // not read when there is no vector
+  for (; i + 3 * stride < vecs; i += 4 * stride) {
     Oct<T> v[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) v[u].load(x + i + u * stride);
+    for (int u = 0; u < 4; ++u) v[u].load(last - (i + u * stride) * kOct);
 #pragma unroll
     for (int u = 0; u < 4; ++u) take(v[u]);
   }
-  for (; i + kOct <= n; i += stride) {
+  for (; i < vecs; i += stride) {
     Oct<T> v;
-    v.load(x + i);
+    v.load(last - i * kOct);
     take(v);
   }
-  for (size_t j = i; j < n && j < i + kOct; ++j) a = max(a, __float_as_uint(static_cast<float>(x[j])) & 0x7fffffffu);
   a = __reduce_max_sync(0xffffffffu, a);
   __shared__ uint32_t part[kMaxBlock / 32];
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = a;
@@ -838,15 +847,18 @@ extern "C" sv_status sv_mx_global_scale(const void* x, long long n, sv_dtype dt,
   const long long per = static_cast<long long>(kMaxBlock) * kOct * 4;
   const long long want = n <= 8 * per ? 1 : (n + per - 1) / per;
   const unsigned blocks = static_cast<unsigned>(want < 4ll * sms ? want : 4ll * sms);
+  cudaLaunchAttribute at;
   if (blocks > 1) {
-    const cudaError_t e = cudaMemsetAsync(g, 0, sizeof(float), st);
-    if (e != cudaSuccess) return launched(e, "tensor scale");
+    const cudaLaunchConfig_t cfg = pdl_config(dim3(1), dim3(1), st, &at);
+    MX_TRY(launched(cudaLaunchKernelEx(&cfg, zero_scale_kernel, g), "tensor scale"));
   }
-  if (dt == SV_BF16)
-    global_scale_kernel<<<blocks, kMaxBlock, 0, st>>>(static_cast<const __nv_bfloat16*>(x), static_cast<size_t>(n), g);
-  else
-    global_scale_kernel<<<blocks, kMaxBlock, 0, st>>>(static_cast<const float*>(x), static_cast<size_t>(n), g);
-  return launched(cudaGetLastError(), "tensor scale");
+  const cudaLaunchConfig_t cfg = pdl_config(dim3(blocks), dim3(kMaxBlock), st, &at);
+  const cudaError_t e =
+      dt == SV_BF16 ? cudaLaunchKernelEx(&cfg, global_scale_kernel<__nv_bfloat16>, static_cast<const __nv_bfloat16*>(x),
+                                         static_cast<size_t>(n), g)
+                    : cudaLaunchKernelEx(&cfg, global_scale_kernel<float>, static_cast<const float*>(x),
+                                         static_cast<size_t>(n), g);
+  return launched(e, "tensor scale");
 }
 
 extern "C" sv_status sv_mx_quantize(const void* x, int B, int H, int N, int D, sv_dtype dt, const sv_mx* out,
