@@ -312,8 +312,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 ? static_cast<long long>(g.runs) * C::kRunCycles / (kEpiWarps * kRounds) * kPace / 16
                                 : 0;
       const int b0 = kQKV ? row0 / g.N : 0, tok0 = kQKV ? row0 - b0 * g.N : row0;
-      // one bulk store takes the warp's 32 rows, unless they run into the next batch
-      const bool bulk = CTAS == 2 && (!kQKV || tok0 + 32 <= g.N);
+      // one bulk store takes the warp's 32 rows (clipped at the last token), unless they run into the next batch
+      const bool bulk = CTAS == 2 && (!kQKV || tok0 + min(32, g.rows - row0) <= g.N);
       // Everything this warp owns goes to registers at once, and the accumulator is free: TMEM reads stall
       // the tensor cores (about 1700 cycles a tile when spread over the next tile's MMAs), and here all
       // four quarters are read at the same time, with one accumulator while the MMAs wait anyway.
