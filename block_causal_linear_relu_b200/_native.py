@@ -512,13 +512,17 @@ class MxTensor:
             device = gscale.device if gscale is not None else torch.device("cuda", torch.cuda.current_device())
         else:
             device = torch.device(device)
+        return cls._new(rows, cols, fmt, gscale, device)
+
+    @classmethod
+    def _new(cls, rows, cols, fmt, gscale, device):
         _mx_check(rows, cols, fmt, gscale, device)
         m = cls.__new__(cls)
         n, ns = _mx_sizes(rows, cols, fmt)  # one allocation; codes and scales are views made when asked for
         m._codes = m._scales = None
-        m._buf = torch.empty(n + ns, dtype=torch.uint8, device=device)
-        p = m._buf.data_ptr()
-        m._set(rows, cols, fmt, gscale, m._buf.device, p, p + n)
+        m._buf = buf = torch.empty(n + ns, dtype=torch.uint8, device=device)
+        p = buf.data_ptr()
+        m._set(rows, cols, fmt, gscale, buf.device, p, p + n)
         return m
 
     @property
@@ -542,9 +546,12 @@ def _mx_check(rows, cols, fmt, gscale, device):
         raise ValueError("fmt must be SV_MXFP8, SV_MXFP4 or SV_NVFP4")
     if rows < 1 or cols < 32 or cols % 32 != 0:
         raise ValueError("rows must be >= 1 and cols a positive multiple of 32")
-    if (gscale is None) != (fmt != SV_NVFP4):
-        raise ValueError("SV_NVFP4 needs a tensor scale gscale; the other formats take none")
-    if gscale is not None and (gscale.dtype != torch.float32 or gscale.numel() != 1 or gscale.device != device):
+    if gscale is None:
+        if fmt == SV_NVFP4:
+            raise ValueError("SV_NVFP4 needs a tensor scale gscale")
+    elif fmt != SV_NVFP4:
+        raise ValueError("only SV_NVFP4 takes a tensor scale")
+    elif (gscale.dtype != torch.float32 or gscale.numel() != 1 or gscale.device != device):
         raise ValueError("gscale must be a float32 tensor of one value on codes' device")
 
 
@@ -552,7 +559,7 @@ def _call(fn, device, stream, *args):
     """Calls fn(*args, stream) with `device` current (the framework's tensors may live on another device
     than the current one) and raises on an error."""
     index = device.index
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         st = fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
     else:
         with torch.cuda.device(index):
@@ -565,13 +572,16 @@ def _raw_stream(index):
     return torch.cuda.current_stream(index).cuda_stream
 
 
+_current_device = torch.cuda.current_device
 if hasattr(torch._C, "_cuda_getCurrentRawStream"):  # the same handle without a Stream object
     _raw_stream = torch._C._cuda_getCurrentRawStream
+if hasattr(torch._C, "_cuda_getDevice"):  # the same index; there is a CUDA tensor, so CUDA is initialised
+    _current_device = torch._C._cuda_getDevice
 
 
 def _mx_out(out, rows, cols, fmt, gscale, device):
     if out is None:
-        return MxTensor.empty(rows, cols, fmt, gscale, device)
+        return MxTensor._new(rows, cols, fmt, gscale, device)
     if out.rows != rows or out.cols != cols or out.fmt != fmt or out.device != device:
         raise ValueError(f"out must be a microscaled [{rows}, {cols}] matrix of the call's format on x's device")
     if gscale is not None and gscale is not out.gscale:
@@ -617,7 +627,7 @@ def sv_mx_quantize(x, fmt: int, gscale=None, out: MxTensor | None = None, stream
 def sv_mx_dequantize(xq: MxTensor, dtype=torch.bfloat16, y=None, stream=None):
     """The values of a microscaled matrix as [rows, cols] bfloat16 or float32."""
     if y is None:
-        y = torch.empty((xq.rows, xq.cols), dtype=dtype, device=xq.device)
+        y = torch.empty(xq.rows, xq.cols, dtype=dtype, device=xq.device)
     elif tuple(y.shape) != (xq.rows, xq.cols) or not y.is_contiguous() or y.device != xq.device:
         raise ValueError("y must be a contiguous [rows, cols] tensor on xq's device")
     _call(load().sv_mx_dequantize, xq.device, stream, xq._ref, y.data_ptr(), _dt(y))
@@ -644,16 +654,18 @@ def sv_rmsnorm(x, w, residual=None, eps: float = 1e-6, fmt: int | None = None, g
         h = x
         pr = ph = None
     else:
+        given = (residual,) if h is None else (residual, h)
         h = torch.empty_like(x) if h is None else h
-        for t in (residual, h):
+        for t in given:
             if t is not x and (t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous()):
                 raise ValueError("residual and h must be contiguous tensors of x's shape, dtype and device")
         pr, ph = residual.data_ptr(), h.data_ptr()
     if fmt is None:
         if gscale is not None:
             raise ValueError("gscale goes with fmt=SV_NVFP4")
-        y = torch.empty_like(x) if y is None else y
-        if y.shape != shape or y.dtype != dtype or y.device != device or not y.is_contiguous():
+        if y is None:
+            y = torch.empty_like(x)
+        elif y.shape != shape or y.dtype != dtype or y.device != device or not y.is_contiguous():
             raise ValueError("y must be a contiguous tensor of x's shape, dtype and device")
         py, pq = y.data_ptr(), None
     else:
@@ -690,7 +702,7 @@ def sv_mx_projection(xq: MxTensor, wq: MxTensor, y=None, ws: Workspace | None = 
     _mx_pair(xq, wq)
     device = xq.device
     if y is None:
-        y = torch.empty((xq.rows, wq.rows), dtype=torch.bfloat16, device=device)
+        y = torch.empty(xq.rows, wq.rows, dtype=torch.bfloat16, device=device)
     elif (y.dtype != torch.bfloat16 or y.numel() != xq.rows * wq.rows or y.shape[-1] != wq.rows or not y.is_contiguous()
             or y.device != device):
         raise ValueError("y must be a contiguous bfloat16 tensor of x's rows and w's rows on x's device")
@@ -706,8 +718,9 @@ def sv_mx_qkv_projection(xq: MxTensor, wq: MxTensor, B: int, N: int, H: int, D: 
     _mx_pair(xq, wq)
     shape = (B, H, N, D)
     device = xq.device
-    q, k, v = (torch.empty(shape, dtype=torch.bfloat16, device=device) if t is None else t for t in (q, k, v))
-    for t in (q, k, v):
+    given = [t for t in (q, k, v) if t is not None]
+    q, k, v = (torch.empty(B, H, N, D, dtype=torch.bfloat16, device=device) if t is None else t for t in (q, k, v))
+    for t in given:
         if t.shape != shape or t.dtype != torch.bfloat16 or not t.is_contiguous() or t.device != device:
             raise ValueError("q, k, v must be contiguous bfloat16 [B, H, N, D] tensors on x's device")
     ws = ws if ws is not None else _mx_workspace(device, stream)

@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(kMxThreads, 4) quantize_kernel(const T* __rest
 }
 
 // value = element * scale (exact in fp32) * g, rounded once to T; kValueUnroll octets of the (row, octet) grid
-// per thread.
+// per thread. Bound by HBM: 20240 x 2560 SV_NVFP4 to bf16 22.2 us, 6.0 TB/s.
 template <int FMT, typename T>
 __global__ void __launch_bounds__(kMxThreads) dequantize_kernel(const uint8_t* __restrict__ codes,
                                                                 const uint8_t* __restrict__ scales, const float* gscale,
@@ -538,7 +538,8 @@ __global__ void __launch_bounds__(kMaxBlock) global_scale_kernel(const T* __rest
 // their uses the 720p prefill took 292 us, bound by their latency). Squares are summed in fp64: then
 // 1 / sqrt(mean + eps), rounded to fp32, does not depend on how the row is split over threads (but for one
 // case in about 1e8), and quantised outputs, where a last-bit difference can move an element by a whole
-// step, do not either.
+// step, do not either. 55200 x 2560 bf16 with a residual: 164 us plain (1.13 GB, 6.9 TB/s: HBM bounds it), 163 us
+// to SV_MXFP8, 170 us to SV_NVFP4.
 constexpr int kPlain = -1;
 constexpr int kMaxTeam = 512;
 
