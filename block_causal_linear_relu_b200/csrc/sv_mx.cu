@@ -35,6 +35,21 @@ constexpr int kMxThreads = 256;  // threads of the quantising and dequantising k
 // steps per thread of the second, all loaded before one is used; the first takes two or four (below)
 constexpr int kValueUnroll = 4;
 
+// two products in one instruction
+__device__ __forceinline__ void mul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\t"
+      "mov.b64 {%0, %1}, d;\n\t}\n"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+template <int E>
+__device__ __forceinline__ void scaled(float (&d)[E], const float* v, float r) {
+#pragma unroll
+  for (int i = 0; i < E; i += 2) mul2(d[i], d[i + 1], v[i], v[i + 1], r, r);
+}
+
 // ---- eight columns as loaded (16-byte aligned) ----
 template <typename T>
 struct Oct;
@@ -51,6 +66,16 @@ struct Oct<__nv_bfloat16> {
       f[2 * i] = __uint_as_float(u[i] << 16);
       f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
     }
+  }
+  // The sum, rounded to bf16: the instruction rounds the exact sum once. (So does an addition in fp32 that
+  // is rounded afterwards: where the fp32 sum is inexact, one of the two is below 2^-16 of the other.)
+  __device__ __forceinline__ void add(const Oct& q) {
+    r.x = add2(r.x, q.r.x), r.y = add2(r.y, q.r.y), r.z = add2(r.z, q.r.z), r.w = add2(r.w, q.r.w);
+  }
+  static __device__ __forceinline__ uint32_t add2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
   }
   __device__ __forceinline__ void set(const float (&f)[8]) {  // rounded
     r = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
@@ -70,6 +95,10 @@ struct Oct<float> {
   }
   __device__ __forceinline__ void get(float (&f)[8]) const {
     f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  }
+  __device__ __forceinline__ void add(const Oct& q) {
+    a.x += q.a.x, a.y += q.a.y, a.z += q.a.z, a.w += q.a.w;
+    b.x += q.b.x, b.y += q.b.y, b.z += q.b.z, b.w += q.b.w;
   }
   __device__ __forceinline__ void set(const float (&f)[8]) {
     a = make_float4(f[0], f[1], f[2], f[3]);
@@ -92,6 +121,10 @@ struct Cols {
   __device__ __forceinline__ void store(T* p) const {
 #pragma unroll
     for (int i = 0; i < E / 8; ++i) o[i].store(p + 8 * i);
+  }
+  __device__ __forceinline__ void add(const Cols& q) {
+#pragma unroll
+    for (int i = 0; i < E / 8; ++i) o[i].add(q.o[i]);
   }
   __device__ __forceinline__ void get(float (&f)[E]) const {
 #pragma unroll
@@ -211,7 +244,7 @@ __device__ __forceinline__ TensorScale tensor_scale(float g) {
 __device__ __forceinline__ uint32_t amax16(const float (&f)[16]) {
   float a = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(fabsf(f[i])));
+  for (int i = 0; i < 16; i += 2) asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(a) : "f"(fabsf(f[i])), "f"(fabsf(f[i + 1])));
   return __float_as_uint(a);
 }
 // The same of 16 columns as loaded.
@@ -274,18 +307,14 @@ __device__ __forceinline__ uint32_t quantise16(const float (&f)[16], uint32_t am
       const float* v = f + 8 * h;
       if (kBf16) {
         float q[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = v[i] * r;
+        scaled(q, v, r);
         code[h] = cvt_e2m1x8(q);
       }
       if (near) {
         const float rl = r * (1.0f - 0x1p-20f), rh = r * (1.0f + 0x1p-20f);
         float lo[8], hi[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          lo[i] = v[i] * rl;
-          hi[i] = v[i] * rh;
-        }
+        scaled(lo, v, rl);
+        scaled(hi, v, rh);
         code[h] = cvt_e2m1x8(lo);
         if (!ts.fits || code[h] != cvt_e2m1x8(hi))
           code[h] = e2m1x8_exact(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7],
@@ -302,8 +331,7 @@ __device__ __forceinline__ uint32_t quantise16(const float (&f)[16], uint32_t am
     const bool bad = ab >= kInfBits;
     const float r = pow2f_bits(bad ? 0 : -k);
     float q[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) q[i] = f[i] * r;
+    scaled(q, f, r);
     if (FMT == SV_MXFP8) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) code[i] = bad ? 0u : cvt_e4m3x4(q + 4 * i);
@@ -581,14 +609,7 @@ __global__ void __launch_bounds__(kMaxTeam)
       if (real && c < cols) r[i].load(res + base + c);
     }
 #pragma unroll
-    for (int i = 0; i < O; ++i) {
-      float f[E], q[E];
-      h[i].get(f);
-      r[i].get(q);
-#pragma unroll
-      for (int j = 0; j < E; ++j) f[j] += q[j];
-      h[i].set(f);
-    }
+    for (int i = 0; i < O; ++i) h[i].add(r[i]);
   }
   double s0 = 0.0, s1 = 0.0;
 #pragma unroll
@@ -624,10 +645,10 @@ __global__ void __launch_bounds__(kMaxTeam)
 #pragma unroll
       for (int j = 0; j < E; j += 4) {
         const float4 ww = __ldg(reinterpret_cast<const float4*>(w + c + j));
-        f[j] = f[j] * rstd * ww.x;
-        f[j + 1] = f[j + 1] * rstd * ww.y;
-        f[j + 2] = f[j + 2] * rstd * ww.z;
-        f[j + 3] = f[j + 3] * rstd * ww.w;
+        mul2(f[j], f[j + 1], f[j], f[j + 1], rstd, rstd);
+        mul2(f[j + 2], f[j + 3], f[j + 2], f[j + 3], rstd, rstd);
+        mul2(f[j], f[j + 1], f[j], f[j + 1], ww.x, ww.y);
+        mul2(f[j + 2], f[j + 3], f[j + 2], f[j + 3], ww.z, ww.w);
       }
     }
     if constexpr (FMT == kPlain) {

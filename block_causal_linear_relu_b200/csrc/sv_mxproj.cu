@@ -9,14 +9,16 @@
 // A persistent kernel of CTA pairs (cta_group::2): an output tile has 256 rows and NT columns; each CTA of
 // a pair holds 128 rows of A and NT / 2 of B in its shared memory, and the pair's MMA reads both, so a
 // byte of shared memory feeds twice the products that it would in one CTA (with 128 x 128 tiles of one
-// CTA the 4-bit kinds need the whole 128 bytes per cycle of shared memory). Few rows take 128 x 64 tiles
-// of single CTAs: then the weight's stream bounds the call, and more CTAs stream faster.
+// CTA the 4-bit kinds need the whole 128 bytes per cycle of shared memory). Few output tiles take
+// 128 x 128 tiles of single CTAs, and a cluster of up to eight of them splits a tile's K: a run costs a CTA
+// about 450 cycles of issue however few rows it has, so a token's latency is runs per CTA. The partial
+// sums meet in distributed shared memory and are added in the order of the ranks.
 // A stage holds a 128-byte run of A and B (128-byte swizzle) and their scale tiles (512 bytes per four
 // blocks of K, stored in the order in which TMEM wants them). Warp 0 of each CTA issues the copies; warp 1
-// of the even CTA copies a stage's scales to TMEM and issues its four MMAs into one of two fp32
-// accumulators; warps 2-5 of each CTA drain the other: the tensor scales, bf16, ReLU, a swizzled buffer,
-// and row-coalesced 16-byte stores. A tile's rows are consecutive rows of X, whatever batch they belong
-// to, because the scale tiles run over all rows; the stores find each row's batch and token.
+// (of a pair's even CTA) copies a stage's scales to TMEM and issues its four MMAs; warps 2-9 of each CTA
+// drain the accumulator: the tensor scales, bf16, ReLU, a swizzled buffer, and a bulk store of 32 rows x 64
+// columns (row by row where those run into another batch). A tile's rows are consecutive rows of X,
+// whatever batch they belong to, because the scale tiles run over all rows.
 // Measured (20240 x 2560 x 7680): SV_NVFP4 160 us, 4975 TFLOP/s (three quarters of four times the measured
 // bf16 rate), SV_MXFP8 281 us, 2840 TFLOP/s (0.86 of twice it). What bounds the 4-bit kinds is the
 // accumulator's way out of TMEM, which stalls the MMAs (a tile's 5120 MMA cycles take 7400), and long
