@@ -406,7 +406,7 @@ struct Walk {
 // they fill the device (20240 x 2560, heads: 30.7 us; two steps 35.1, four in 97 registers 40.2; a block of
 // 2760 rows: 6.7 and 5.7 us). The conversions to e2m1 (8 cycles a pair and warp) bound it there.
 template <int FMT, typename T, bool kHeads, int kSteps>
-__global__ void __launch_bounds__(kMxThreads, 4) quantize_kernel(const T* __restrict__ x, int H, FastDiv N, FastDiv D,
+__global__ void __launch_bounds__(kMxThreads, FMT == SV_NVFP4 ? 4 : 6) quantize_kernel(const T* __restrict__ x, int H, FastDiv N, FastDiv D,
                                                               uint32_t rows, int cols, Walk walk, int sp,
                                                               uint32_t rows_padded, const float* gscale, uint8_t* codes,
                                                               uint8_t* scales) {
