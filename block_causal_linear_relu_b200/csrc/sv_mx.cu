@@ -1,9 +1,10 @@
 // Microscaled operands, sm_100a: quantisation to block-scaled 8- and 4-bit floating point, the way
 // back, the tensor scale, and the root-mean-square norm whose output is quantised in the same pass.
 //
-// All of it is bound by HBM: a pass reads each input once and writes codes and scales once. A thread
-// holds octets of columns in registers (16 bytes of bf16: coalesced loads and stores), and a block is two
-// (SV_NVFP4) or four neighbouring lanes, so its largest magnitude takes one or two shuffles.
+// A pass reads each input once and writes codes and scales once, and HBM bounds all but the quantisation to
+// SV_NVFP4, which its arithmetic bounds. Where a thread quantises it holds 16 consecutive columns, one
+// SV_NVFP4 block or half an MX block whose other half is in the neighbouring lane, so that a block's scale
+// is worked out once or twice; elsewhere it holds eight (16 bytes of bf16: coalesced loads and stores).
 //
 // Rounding. An element is x / s (or x / (s g)) rounded once, to nearest even. For the MX formats s is
 // a power of two and the product x * 2^-k is exact, so the conversion instruction rounds correctly.
@@ -406,10 +407,9 @@ struct Walk {
 // they fill the device (20240 x 2560, heads: 30.7 us; two steps 35.1, four in 97 registers 40.2; a block of
 // 2760 rows: 6.7 and 5.7 us). The conversions to e2m1 (8 cycles a pair and warp) bound it there.
 template <int FMT, typename T, bool kHeads, int kSteps>
-__global__ void __launch_bounds__(kMxThreads, FMT == SV_NVFP4 ? 4 : 6) quantize_kernel(const T* __restrict__ x, int H, FastDiv N, FastDiv D,
-                                                              uint32_t rows, int cols, Walk walk, int sp,
-                                                              uint32_t rows_padded, const float* gscale, uint8_t* codes,
-                                                              uint8_t* scales) {
+__global__ void __launch_bounds__(kMxThreads, FMT == SV_NVFP4 ? 4 : 6)
+    quantize_kernel(const T* __restrict__ x, int H, FastDiv N, FastDiv D, uint32_t rows, int cols, Walk walk, int sp,
+                    uint32_t rows_padded, const float* gscale, uint8_t* codes, uint8_t* scales) {
   uint32_t row;
   int grp;
   walk.start(static_cast<size_t>(blockIdx.x) * (kMxThreads * kSteps) + threadIdx.x, row, grp);
@@ -503,17 +503,17 @@ __global__ void __launch_bounds__(kMxThreads) dequantize_kernel(const uint8_t* _
   }
 }
 
-// *g = max over the grid of max |x_i| / 2688. The quotient of non-negative values grows with |x|, so
-// the maximum of the blocks' quotients (as integers: the bits of non-negative floats are ordered, NaN
-// above all) is the quotient of the maximum, in any order. *g is zeroed before the launch, but for one block,
-// which stores its result. Four vectors per thread and step, so that enough bytes are in flight; from the
-// end to the start, so that the quantisation that follows finds the first part of x in L2.
 __global__ void zero_scale_kernel(float* g) {  // instead of a memset: the next launch overlaps with it
   griddep_launch_dependents();
   griddep_wait();
   *g = 0.f;
 }
 
+// *g = max over the grid of max |x_i| / 2688. The quotient of non-negative values grows with |x|, so
+// the maximum of the blocks' quotients (as integers: the bits of non-negative floats are ordered, NaN
+// above all) is the quotient of the maximum, in any order. *g is zeroed before the launch, but for one block,
+// which stores its result. Four vectors per thread and step, so that enough bytes are in flight: 104 MB of
+// bf16 17.5 us with the zeroing, 5.9 TB/s.
 constexpr int kMaxBlock = 512;
 template <typename T>
 __global__ void __launch_bounds__(kMaxBlock) global_scale_kernel(const T* __restrict__ x, size_t n, float* g) {
@@ -529,17 +529,16 @@ __global__ void __launch_bounds__(kMaxBlock) global_scale_kernel(const T* __rest
     for (int j = 0; j < 8; ++j) a = max(a, __float_as_uint(f[j]) & 0x7fffffffu);
   };
   if (i < n % kOct) a = __float_as_uint(static_cast<float>(x[vecs * kOct + i])) & 0x7fffffffu;
-  const T* last = x + (vecs - 1) * kOct;  // not read when there is no vector
   for (; i + 3 * stride < vecs; i += 4 * stride) {
     Oct<T> v[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) v[u].load(last - (i + u * stride) * kOct);
+    for (int u = 0; u < 4; ++u) v[u].load(x + (i + u * stride) * kOct);
 #pragma unroll
     for (int u = 0; u < 4; ++u) take(v[u]);
   }
   for (; i < vecs; i += stride) {
     Oct<T> v;
-    v.load(last - i * kOct);
+    v.load(x + i * kOct);
     take(v);
   }
   a = __reduce_max_sync(0xffffffffu, a);
@@ -560,14 +559,14 @@ __global__ void __launch_bounds__(kMaxBlock) global_scale_kernel(const T* __rest
 
 // ---- norm ----
 // A team of blockDim.x threads takes one row (blockDim.y rows per block; more than one only with teams of at
-// most a warp: 8, 16 or 32 lanes). Thread t holds the column groups i * blockDim.x + t, i < O, of E columns (8, or 16 where
-// they are quantised) in registers from the load to the store, so x and the residual are read once; all
+// most a warp: 8, 16 or 32 lanes). Thread t holds the column groups i * blockDim.x + t, i < O, of E columns
+// (8, or 16 where they are quantised) in registers from the load to the store, so x and the residual are read once; all
 // loads are issued before the first is used (with the unpacked values in registers and loads between
 // their uses the 720p prefill took 292 us, bound by their latency). Squares are summed in fp64: then
 // 1 / sqrt(mean + eps), rounded to fp32, does not depend on how the row is split over threads (but for one
 // case in about 1e8), and quantised outputs, where a last-bit difference can move an element by a whole
-// step, do not either. 55200 x 2560 bf16 with a residual: 164 us plain (1.13 GB, 6.9 TB/s: HBM bounds it), 163 us
-// to SV_MXFP8, 170 us to SV_NVFP4.
+// step, do not either. 55200 x 2560 bf16 with a residual: 164 us plain (1.13 GB, 6.9 TB/s: HBM bounds it),
+// 160 us to SV_MXFP8, 166 us to SV_NVFP4.
 constexpr int kPlain = -1;
 constexpr int kMaxTeam = 512;
 
@@ -660,7 +659,8 @@ __global__ void __launch_bounds__(kMaxTeam)
     } else {
       uint32_t code[4];
       const uint32_t sb = quantise16<FMT, false>(f, amax16(f), ts, code);
-      put16<FMT>(codes, scales, row, grp, cols, sp, grp < gp && row < rows_padded, live, code, sb);  // the team may cover more than gp groups
+      // the team may cover more than gp groups
+      put16<FMT>(codes, scales, row, grp, cols, sp, grp < gp && row < rows_padded, live, code, sb);
     }
   }
 }

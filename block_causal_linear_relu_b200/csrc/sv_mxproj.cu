@@ -110,11 +110,10 @@ __device__ __forceinline__ size_t offset(const Geo& g, const Place& p, int row) 
   const int b = row / g.N;
   return ((static_cast<size_t>(b) * g.H + p.h) * g.N + (row - b * g.N)) * g.D + p.d;
 }
-__device__ __forceinline__ __nv_bfloat16* output(const Ops& op, int t) { return t == 0 ? op.o0 : (t == 1 ? op.o1 : op.o2); }
+__device__ __forceinline__ __nv_bfloat16* output(const Ops& op, int t) {
+  return t == 0 ? op.o0 : (t == 1 ? op.o1 : op.o2);
+}
 
-// Tiles are numbered column tile fastest: the CTAs at work share a few row tiles of A (read from DRAM once)
-// and sweep W, which stays in L2. Blocks of 4 or 8 row tiles, which touch fewer distinct tiles at a time,
-// measured 2.5 and 5 % slower on the 720p Q/K/V projection.
 __device__ __forceinline__ bool warp_all(bool ok) { return __all_sync(0xffffffffu, ok); }
 
 template <int FMT, int CTAS, int NT, bool kQKV>
@@ -132,6 +131,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int rank = CTAS == 2 ? static_cast<int>(cluster_ctarank()) : 0;
+  // Tiles are numbered column tile fastest: the CTAs at work share a few row tiles of A (read from DRAM once)
+  // and sweep W, which stays in L2. Blocks of 4 or 8 row tiles, which touch fewer distinct tiles at a time,
+  // measured 2.5 and 5 % slower on the 720p Q/K/V projection.
   const int group = CTAS == 2 ? 2 : g.split;  // CTAs that work on one tile
   const int first = static_cast<int>(blockIdx.x) / group, step = static_cast<int>(gridDim.x) / group;
   const int krank = CTAS == 1 && g.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
