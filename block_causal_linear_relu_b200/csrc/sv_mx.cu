@@ -513,7 +513,8 @@ __global__ void zero_scale_kernel(float* g) {  // instead of a memset: the next 
 // the maximum of the blocks' quotients (as integers: the bits of non-negative floats are ordered, NaN
 // above all) is the quotient of the maximum, in any order. *g is zeroed before the launch, but for one block,
 // which stores its result. Four vectors per thread and step, so that enough bytes are in flight: 104 MB of
-// bf16 17.5 us with the zeroing, 5.9 TB/s.
+// bf16 17.5 us with the zeroing, 5.9 TB/s. From the end to the start: the quantisation that follows then
+// finds the first part of x in L2 (an fp32 weight to SV_NVFP4 and back 41.0 -> 39.7 us).
 constexpr int kMaxBlock = 512;
 template <typename T>
 __global__ void __launch_bounds__(kMaxBlock) global_scale_kernel(const T* __restrict__ x, size_t n, float* g) {
@@ -532,13 +533,13 @@ __global__ void __launch_bounds__(kMaxBlock) global_scale_kernel(const T* __rest
   for (; i + 3 * stride < vecs; i += 4 * stride) {
     Oct<T> v[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) v[u].load(x + (i + u * stride) * kOct);
+    for (int u = 0; u < 4; ++u) v[u].load(x + (vecs - 1 - i - u * stride) * kOct);
 #pragma unroll
     for (int u = 0; u < 4; ++u) take(v[u]);
   }
   for (; i < vecs; i += stride) {
     Oct<T> v;
-    v.load(x + i * kOct);
+    v.load(x + (vecs - 1 - i) * kOct);
     take(v);
   }
   a = __reduce_max_sync(0xffffffffu, a);
