@@ -474,7 +474,7 @@ def _mx_scale_shape(rows, cols, fmt):
 def _mx_sizes(rows, cols, fmt):
     """(bytes of codes rounded up to 256, bytes of scales)."""
     run = _MX_RUN[fmt]
-    return ((rows * cols >> (fmt != SV_MXFP8)) + 255 & -256,
+    return ((rows * cols if fmt == SV_MXFP8 else rows * cols // 2) + 255 & -256,
             (rows + 127 & -128) * (-(-cols // run) * (run // _MX_BLOCK[fmt])))
 
 
@@ -498,11 +498,8 @@ class MxTensor:
                 or scales.device != codes.device):
             raise ValueError(f"scales must be a contiguous uint8 tensor {_mx_scale_shape(rows, cols, fmt)} on codes' device")
         self._codes, self._scales, self._buf = codes, scales, None
-        self._set(rows, cols, fmt, gscale, codes.device, codes.data_ptr(), scales.data_ptr())
-
-    def _set(self, rows, cols, fmt, gscale, device, codes, scales):
-        self.rows, self.cols, self.fmt, self.gscale, self.device = rows, cols, fmt, gscale, device
-        self._c = SvMx(codes, scales, None if gscale is None else gscale.data_ptr(), rows, cols, fmt)
+        self.rows, self.cols, self.fmt, self.gscale, self.device = rows, cols, fmt, gscale, codes.device
+        self._c = SvMx(codes.data_ptr(), scales.data_ptr(), None if gscale is None else gscale.data_ptr(), rows, cols, fmt)
         self._ref = ctypes.byref(self._c)
 
     @classmethod
@@ -519,10 +516,12 @@ class MxTensor:
         _mx_check(rows, cols, fmt, gscale, device)
         m = cls.__new__(cls)
         n, ns = _mx_sizes(rows, cols, fmt)  # one allocation; codes and scales are views made when asked for
-        m._codes = m._scales = None
         m._buf = buf = torch.empty(n + ns, dtype=torch.uint8, device=device)
+        m._codes = m._scales = None
+        m.rows, m.cols, m.fmt, m.gscale, m.device = rows, cols, fmt, gscale, buf.device
         p = buf.data_ptr()
-        m._set(rows, cols, fmt, gscale, buf.device, p, p + n)
+        m._c = c = SvMx(p, p + n, None if gscale is None else gscale.data_ptr(), rows, cols, fmt)
+        m._ref = ctypes.byref(c)
         return m
 
     @property
@@ -555,17 +554,23 @@ def _mx_check(rows, cols, fmt, gscale, device):
         raise ValueError("gscale must be a float32 tensor of one value on codes' device")
 
 
-def _call(fn, device, stream, *args):
-    """Calls fn(*args, stream) with `device` current (the framework's tensors may live on another device
-    than the current one) and raises on an error."""
-    index = device.index
+def _call(fn, index, args):
+    """fn(*args) with device `index` current (tensors may live on another device than the current one);
+    raises on an error."""
     if index == _current_device():
-        st = fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
+        st = fn(*args)
     else:
         with torch.cuda.device(index):
-            st = fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
+            st = fn(*args)
     if st != SV_OK:
         _check(st)
+
+
+def _made(t, stream):
+    """A tensor that a call allocated (on the current stream) and that `stream`, if given, writes."""
+    if stream is not None:
+        t.record_stream(stream)
+    return t
 
 
 def _raw_stream(index):
@@ -579,9 +584,12 @@ if hasattr(torch._C, "_cuda_getDevice"):  # the same index; there is a CUDA tens
     _current_device = torch._C._cuda_getDevice
 
 
-def _mx_out(out, rows, cols, fmt, gscale, device):
+def _mx_out(out, rows, cols, fmt, gscale, device, stream):
     if out is None:
-        return MxTensor._new(rows, cols, fmt, gscale, device)
+        out = MxTensor._new(rows, cols, fmt, gscale, device)
+        if stream is not None:
+            out._buf.record_stream(stream)
+        return out
     if out.rows != rows or out.cols != cols or out.fmt != fmt or out.device != device:
         raise ValueError(f"out must be a microscaled [{rows}, {cols}] matrix of the call's format on x's device")
     if gscale is not None and gscale is not out.gscale:
@@ -589,48 +597,53 @@ def _mx_out(out, rows, cols, fmt, gscale, device):
     return out
 
 
-def _dense(x, name):
+def _dense(x):
     if not x.is_cuda or not x.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+        raise ValueError("x must be a contiguous CUDA tensor")
 
 
 def sv_mx_global_scale(x, g=None, stream=None):
     """The tensor scale of SV_NVFP4: max |x| / (6 * 448) as a float32 tensor [1] (g, when given)."""
-    _dense(x, "x")
+    _dense(x)
     device = x.device
+    index = device.index
     if g is None:
-        g = torch.empty(1, dtype=torch.float32, device=device)
+        g = _made(torch.empty(1, dtype=torch.float32, device=device), stream)
     elif g.dtype != torch.float32 or g.numel() != 1 or g.device != device:
         raise ValueError("g must be a float32 tensor of one value on x's device")
-    _call(load().sv_mx_global_scale, device, stream, x.data_ptr(), x.numel(), _dt(x), g.data_ptr())
+    _call(load().sv_mx_global_scale, index, (x.data_ptr(), x.numel(), _dt(x), g.data_ptr(),
+                                             _raw_stream(index) if stream is None else stream.cuda_stream))
     return g
 
 
 def sv_mx_quantize(x, fmt: int, gscale=None, out: MxTensor | None = None, stream=None) -> MxTensor:
     """x to a microscaled matrix: [..., C] rows as they are, or [B, H, N, D] (four dimensions) as B * N
     rows that hold the heads side by side. SV_NVFP4 takes the tensor scale gscale (float32 [1])."""
-    _dense(x, "x")
-    shape = x.shape
-    if len(shape) < 2:
-        raise ValueError("x must be [..., C] or [B, H, N, D]")
+    _dense(x)
+    shape, device = x.shape, x.device
+    index = device.index
     if len(shape) == 4:
         B, H, N, D = shape
-    else:
+    elif len(shape) >= 2:
         B, H, D = 1, 1, shape[-1]
         N = x.numel() // D if D else 0
-    device = x.device
-    out = _mx_out(out, B * N, H * D, fmt, gscale, device)
-    _call(load().sv_mx_quantize, device, stream, x.data_ptr(), B, H, N, D, _dt(x), out._ref)
+    else:
+        raise ValueError("x must be [..., C] or [B, H, N, D]")
+    out = _mx_out(out, B * N, H * D, fmt, gscale, device, stream)
+    _call(load().sv_mx_quantize, index, (x.data_ptr(), B, H, N, D, _dt(x), out._ref,
+                                         _raw_stream(index) if stream is None else stream.cuda_stream))
     return out
 
 
 def sv_mx_dequantize(xq: MxTensor, dtype=torch.bfloat16, y=None, stream=None):
     """The values of a microscaled matrix as [rows, cols] bfloat16 or float32."""
+    index = xq.device.index
     if y is None:
-        y = torch.empty(xq.rows, xq.cols, dtype=dtype, device=xq.device)
+        y = _made(torch.empty(xq.rows, xq.cols, dtype=dtype, device=xq.device), stream)
     elif tuple(y.shape) != (xq.rows, xq.cols) or not y.is_contiguous() or y.device != xq.device:
         raise ValueError("y must be a contiguous [rows, cols] tensor on xq's device")
-    _call(load().sv_mx_dequantize, xq.device, stream, xq._ref, y.data_ptr(), _dt(y))
+    _call(load().sv_mx_dequantize, index, (xq._ref, y.data_ptr(), _dt(y),
+                                           _raw_stream(index) if stream is None else stream.cuda_stream))
     return y
 
 
@@ -640,8 +653,9 @@ def sv_rmsnorm(x, w, residual=None, eps: float = 1e-6, fmt: int | None = None, g
     h = x + residual in x's dtype (x itself without a residual). y = h / rms(h) * w, in x's dtype and shape,
     or, with fmt, quantised in the same pass to an MxTensor of one row per position (y, when given, is that
     MxTensor; SV_NVFP4 takes gscale). h may be x or residual (in place)."""
-    _dense(x, "x")
+    _dense(x)
     shape, dtype, device = x.shape, x.dtype, x.device
+    index = device.index
     C = shape[-1] if len(shape) else 0
     rows = x.numel() // C if C else 0
     if rows == 0:
@@ -654,24 +668,24 @@ def sv_rmsnorm(x, w, residual=None, eps: float = 1e-6, fmt: int | None = None, g
         h = x
         pr = ph = None
     else:
-        given = (residual,) if h is None else (residual, h)
-        h = torch.empty_like(x) if h is None else h
-        for t in given:
+        for t in (residual,) if h is None else (residual, h):
             if t is not x and (t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous()):
                 raise ValueError("residual and h must be contiguous tensors of x's shape, dtype and device")
+        h = _made(torch.empty_like(x), stream) if h is None else h
         pr, ph = residual.data_ptr(), h.data_ptr()
     if fmt is None:
         if gscale is not None:
             raise ValueError("gscale goes with fmt=SV_NVFP4")
         if y is None:
-            y = torch.empty_like(x)
+            y = _made(torch.empty_like(x), stream)
         elif y.shape != shape or y.dtype != dtype or y.device != device or not y.is_contiguous():
             raise ValueError("y must be a contiguous tensor of x's shape, dtype and device")
         py, pq = y.data_ptr(), None
     else:
-        y = _mx_out(y, rows, C, fmt, gscale, device)
+        y = _mx_out(y, rows, C, fmt, gscale, device, stream)
         py, pq = None, y._ref
-    _call(load().sv_rmsnorm, device, stream, x.data_ptr(), pr, ph, w.data_ptr(), rows, C, _dt(x), eps, py, pq)
+    _call(load().sv_rmsnorm, index, (x.data_ptr(), pr, ph, w.data_ptr(), rows, C, _dt(x), eps, py, pq,
+                                     _raw_stream(index) if stream is None else stream.cuda_stream))
     return y, h
 
 
@@ -701,13 +715,15 @@ def sv_mx_projection(xq: MxTensor, wq: MxTensor, y=None, ws: Workspace | None = 
     (or pass ws) before capturing one into a CUDA graph."""
     _mx_pair(xq, wq)
     device = xq.device
+    index = device.index
     if y is None:
-        y = torch.empty(xq.rows, wq.rows, dtype=torch.bfloat16, device=device)
+        y = _made(torch.empty(xq.rows, wq.rows, dtype=torch.bfloat16, device=device), stream)
     elif (y.dtype != torch.bfloat16 or y.numel() != xq.rows * wq.rows or y.shape[-1] != wq.rows or not y.is_contiguous()
             or y.device != device):
         raise ValueError("y must be a contiguous bfloat16 tensor of x's rows and w's rows on x's device")
     ws = ws if ws is not None else _mx_workspace(device, stream)
-    _call(load().sv_mx_projection, device, stream, xq._ref, wq._ref, y.data_ptr(), ws.ptr, ws.nbytes)
+    _call(load().sv_mx_projection, index, (xq._ref, wq._ref, y.data_ptr(), ws.ptr, ws.nbytes,
+                                           _raw_stream(index) if stream is None else stream.cuda_stream))
     return y
 
 
@@ -716,14 +732,18 @@ def sv_mx_qkv_projection(xq: MxTensor, wq: MxTensor, B: int, N: int, H: int, D: 
     """x of B * N rows, w of 3 * H * D rows -> (ReLU(q), ReLU(k), v), each [B, H, N, D] bfloat16. ws as for
     sv_mx_projection."""
     _mx_pair(xq, wq)
-    shape = (B, H, N, D)
     device = xq.device
-    given = [t for t in (q, k, v) if t is not None]
-    q, k, v = (torch.empty(B, H, N, D, dtype=torch.bfloat16, device=device) if t is None else t for t in (q, k, v))
-    for t in given:
-        if t.shape != shape or t.dtype != torch.bfloat16 or not t.is_contiguous() or t.device != device:
+    index = device.index
+    if B * N != xq.rows or 3 * H * D != wq.rows:
+        raise ValueError("x must have B * N rows and w 3 * H * D rows")
+    for t in (q, k, v):
+        if t is not None and (t.shape != (B, H, N, D) or t.dtype != torch.bfloat16 or not t.is_contiguous()
+                              or t.device != device):
             raise ValueError("q, k, v must be contiguous bfloat16 [B, H, N, D] tensors on x's device")
+    q, k, v = (_made(torch.empty(B, H, N, D, dtype=torch.bfloat16, device=device), stream) if t is None else t
+               for t in (q, k, v))
     ws = ws if ws is not None else _mx_workspace(device, stream)
-    _call(load().sv_mx_qkv_projection, device, stream, xq._ref, wq._ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), B, N,
-          H, D, ws.ptr, ws.nbytes)
+    _call(load().sv_mx_qkv_projection, index, (xq._ref, wq._ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), B, N, H, D,
+                                               ws.ptr, ws.nbytes,
+                                               _raw_stream(index) if stream is None else stream.cuda_stream))
     return q, k, v

@@ -475,6 +475,29 @@ def test_two_streams_at_once(sv):
         check_product(y, xv, wv, 512)
 
 
+def test_calls_on_a_given_stream(sv):
+    # every call on a stream that is not the current one, its outputs dropped early
+    side = torch.cuda.Stream()
+    x, r = make((900, 256), "bf16", 46, odd=False), make((900, 256), "bf16", 47, odd=False)
+    w = make((256,), "f32", 48, odd=False)
+    wq, _ = operand(sv, 384, 256, "nvfp4", 49)
+
+    def chain(stream):
+        g = sv.sv_mx_global_scale(x, stream=stream)
+        yq, h = sv.sv_rmsnorm(x, w, residual=r, fmt=sv.SV_NVFP4, gscale=g, stream=stream)
+        q, k, v = sv.sv_mx_qkv_projection(yq, wq, 3, 300, 2, 64, stream=stream)
+        oq = sv.sv_mx_quantize(q, sv.SV_MXFP8, stream=stream)
+        return h, q, k, v, sv.sv_mx_dequantize(oq, stream=stream), sv.sv_mx_projection(yq, wq, stream=stream)
+
+    want = chain(None)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = chain(side)
+        trash = [torch.full((900, 256), 3.0, device="cuda") for _ in range(8)]  # takes what the chain has freed
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)) and len(trash) == 8
+
+
 def test_rows_past_the_end_are_left_as_they_were(sv):
     xq, xv = operand(sv, 130, 128, "mxfp4", 44)
     wq, wv = operand(sv, 72, 128, "mxfp4", 45)
@@ -506,7 +529,7 @@ def test_bad_arguments_raise(sv):
         sv.sv_mx_projection(a, b)
     with pytest.raises(sv.SvError):
         sv.sv_mx_projection(a, sv.sv_mx_quantize(x[:3].contiguous(), sv.SV_MXFP8))  # 3 output features
-    with pytest.raises(sv.SvError):
+    with pytest.raises(ValueError):
         sv.sv_mx_qkv_projection(a, a, 1, 3, 1, 64)
     with pytest.raises(ValueError):
         sv.sv_rmsnorm(x, torch.ones(32, device="cuda"))
