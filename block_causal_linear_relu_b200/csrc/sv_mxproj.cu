@@ -61,12 +61,13 @@ struct Cfg {
   static constexpr int kSmem = kBarOff + 256 + 1024;  // barriers, TMEM slot, alignment slack
   static_assert(CTAS == 2 || (NT == 128 && kStagingOff >= kRows * NT * 4), "a tile's fp32 sums fit into the stages");
   static_assert(kSmem <= 227 * 1024 && kStages >= 4, "shared memory of the microscaled product");
-  // TMEM columns: the accumulators (two of up to 192 columns; two of 256 and the scales do not fit), then two
-  // buffers of scales (A: 4 per tile, B: 4 per tile and block)
+  // TMEM columns: the accumulators (two where they fit), then scales (A: 4 per tile, B: 4 per tile and block), a
+  // buffer for every stage: a stage's buffer is written again only when its shared memory has been loaded
+  // again, that is, after the MMAs that read both have retired.
   static constexpr uint32_t kScaleCols = 4 * kTiles * (1 + kBBlocks);
-  static constexpr int kAccs = 2 * NT + 2 * kScaleCols <= 512 ? 2 : 1;
+  static constexpr int kAccs = 2 * NT + kStages * kScaleCols <= 512 ? 2 : 1;
   static constexpr uint32_t kScaleCol = kAccs * NT;
-  static_assert(kScaleCol + 2 * kScaleCols <= 512, "TMEM columns");
+  static_assert(kScaleCol + kStages * kScaleCols <= 512, "TMEM columns");
   // cycles that a run of K takes: 2 per column on the tensor cores, or its bytes at about 60 per cycle
   static constexpr int kRunCycles = 2 * NT > kStageBytes / 60 ? 2 * NT : kStageBytes / 60;
   static constexpr MxKind kKind = FMT == SV_MXFP8 ? kMx8 : FMT == SV_MXFP4 ? kMx4 : kNv4;
@@ -232,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t a0 = smem_u32(smem) >> 4;
       const uint64_t hi = sdesc_sw128(0, 16, 1024), hi_sc = sdesc_scales(0);
       int s = 0, tl = 0;
-      uint32_t phase = 0, buf = 0, off = 0;
+      uint32_t phase = 0, off = 0;
       bool ok = true, ready = mbar_test(&full[0], 0);
       for (int tile = first; tile < g.tiles && ok; tile += step, ++tl) {
         const int a = tl % C::kAccs;
@@ -248,14 +249,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t da = hi | (a0 + off), db = hi | (a0 + off + (C::kABytes >> 4)),
                          ds = hi_sc | (a0 + off + ((C::kABytes + C::kBBytes) >> 4));
           uint64_t* const done = &empty[s];
+          const uint32_t ta = tmem + C::kScaleCol + static_cast<uint32_t>(s) * C::kScaleCols;
+          const uint32_t tb = ta + 4 * C::kTiles;
           off += C::kStride >> 4;
           if (++s == C::kStages) s = 0, phase ^= 1, off = 0;
           ready = mbar_test(&full[s], phase);
-          // Copies and MMAs of one thread run in order, so a copy into a buffer follows the MMAs that
-          // read it; two buffers let it run beside the MMAs of the run before.
-          const uint32_t ta = tmem + C::kScaleCol + buf * C::kScaleCols;
-          const uint32_t tb = ta + 4 * C::kTiles;
-          buf ^= 1;
           if (issue) {
 #pragma unroll
             for (int t = 0; t < C::kTiles; ++t) {
