@@ -692,10 +692,11 @@ def sv_rmsnorm(x, w, residual=None, eps: float = 1e-6, fmt: int | None = None, g
 _mx_ws = {}
 
 
-def _mx_workspace(device, stream):
-    """The status workspace of the microscaled products, one per device: they use its status word only,
-    so calls on several streams share it."""
-    ws = _mx_ws.get(device.index)
+def _mx_workspace(ws, device, stream):
+    """The caller's workspace, else the products' own, one per device: they use its status word only, so
+    calls on several streams share it. Raises if an earlier call on it timed out."""
+    if ws is None:
+        ws = _mx_ws.get(device.index)
     if ws is None:
         if torch.cuda.is_current_stream_capturing():
             raise RuntimeError("the microscaled products' workspace must exist before a capture: make a call first, or pass ws")
@@ -721,7 +722,7 @@ def sv_mx_projection(xq: MxTensor, wq: MxTensor, y=None, ws: Workspace | None = 
     elif (y.dtype != torch.bfloat16 or y.numel() != xq.rows * wq.rows or y.shape[-1] != wq.rows or not y.is_contiguous()
             or y.device != device):
         raise ValueError("y must be a contiguous bfloat16 tensor of x's rows and w's rows on x's device")
-    ws = ws if ws is not None else _mx_workspace(device, stream)
+    ws = _mx_workspace(ws, device, stream)
     _call(load().sv_mx_projection, index, (xq._ref, wq._ref, y.data_ptr(), ws.ptr, ws.nbytes,
                                            _raw_stream(index) if stream is None else stream.cuda_stream))
     return y
@@ -742,7 +743,7 @@ def sv_mx_qkv_projection(xq: MxTensor, wq: MxTensor, B: int, N: int, H: int, D: 
             raise ValueError("q, k, v must be contiguous bfloat16 [B, H, N, D] tensors on x's device")
     q, k, v = (_made(torch.empty(B, H, N, D, dtype=torch.bfloat16, device=device), stream) if t is None else t
                for t in (q, k, v))
-    ws = ws if ws is not None else _mx_workspace(device, stream)
+    ws = _mx_workspace(ws, device, stream)
     _call(load().sv_mx_qkv_projection, index, (xq._ref, wq._ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), B, N, H, D,
                                                ws.ptr, ws.nbytes,
                                                _raw_stream(index) if stream is None else stream.cuda_stream))

@@ -435,6 +435,39 @@ def test_captured_and_replayed(sv):
             assert torch.equal(a, b)
 
 
+def test_captured_weight_conversion(sv):
+    # the two launches of a large tensor scale are replayed, also when the new maximum is smaller
+    x = make((600, 2560), "f32", 62, odd=False)
+    sv.sv_mx_quantize(x, sv.SV_NVFP4, gscale=sv.sv_mx_global_scale(x))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g = sv.sv_mx_global_scale(x)
+        q = sv.sv_mx_quantize(x, sv.SV_NVFP4, gscale=g)
+        y = sv.sv_mx_dequantize(q)
+    for factor in (1.0, 0.01, 3.0):
+        x.copy_(make((600, 2560), "f32", 63, factor, odd=False))
+        graph.replay()
+        torch.cuda.synchronize()
+        g2 = sv.sv_mx_global_scale(x)
+        assert torch.equal(g, g2)
+        q2 = sv.sv_mx_quantize(x, sv.SV_NVFP4, gscale=g2)
+        assert torch.equal(q.codes, q2.codes) and torch.equal(q.scales, q2.scales)
+        assert torch.equal(y, sv.sv_mx_dequantize(q2))
+
+
+def test_slices_of_whole_row_tiles(sv):
+    # 128 rows are one tile of scales: a matrix can be cut there without a copy
+    for fmt in FMTS:
+        xq, xv = operand(sv, 384, 320, fmt, 64)
+        wq, wv = operand(sv, 256, 320, fmt, 65)
+        part = sv.MxTensor(xq.codes[128:256], xq.scales[1:2], 128, 320, xq.fmt, xq.gscale)
+        half = sv.MxTensor(wq.codes[128:], wq.scales[1:], 128, 320, wq.fmt, wq.gscale)
+        y = sv.sv_mx_projection(part, half)
+        check_product(y, xv[128:256], wv[128:], 320)
+        assert same(f64(sv.sv_mx_dequantize(part, torch.float32)), np.float32(xv[128:256]).astype(np.float64))
+
+
 def test_first_call_inside_a_capture_is_refused(sv):
     from block_causal_linear_relu_b200 import _native
     xq, _ = operand(sv, 16, 64, "mxfp8", 60)
