@@ -512,11 +512,11 @@ class MxTensor:
         return cls._new(rows, cols, fmt, gscale, device)
 
     @classmethod
-    def _new(cls, rows, cols, fmt, gscale, device):
+    def _new(cls, rows, cols, fmt, gscale, device, stream=None):
         _mx_check(rows, cols, fmt, gscale, device)
         m = cls.__new__(cls)
         n, ns = _mx_sizes(rows, cols, fmt)  # one allocation; codes and scales are views made when asked for
-        m._buf = buf = torch.empty(n + ns, dtype=torch.uint8, device=device)
+        m._buf = buf = _made(stream, torch.empty, n + ns, dtype=torch.uint8, device=device)
         m._codes = m._scales = None
         m.rows, m.cols, m.fmt, m.gscale, m.device = rows, cols, fmt, gscale, buf.device
         p = buf.data_ptr()
@@ -566,10 +566,17 @@ def _call(fn, index, args):
         _check(st)
 
 
-def _made(t, stream):
-    """A tensor that a call allocated (on the current stream) and that `stream`, if given, writes."""
-    if stream is not None:
-        t.record_stream(stream)
+def _made(stream, make, *args, **kwargs):
+    """make(*args, **kwargs): a tensor that a call on `stream` (None: the current stream) allocates and writes.
+
+    Its memory belongs to the stream that writes it: memory freed on the current stream may still be read or
+    written there by queued kernels, which a call on another stream does not wait for. The current stream is
+    recorded as one that uses the tensor too, so that it may be read there and dropped without a wait."""
+    if stream is None:
+        return make(*args, **kwargs)
+    with torch.cuda.stream(stream):
+        t = make(*args, **kwargs)
+    t.record_stream(torch.cuda.current_stream(t.device))
     return t
 
 
@@ -586,10 +593,7 @@ if hasattr(torch._C, "_cuda_getDevice"):  # the same index; there is a CUDA tens
 
 def _mx_out(out, rows, cols, fmt, gscale, device, stream):
     if out is None:
-        out = MxTensor._new(rows, cols, fmt, gscale, device)
-        if stream is not None:
-            out._buf.record_stream(stream)
-        return out
+        return MxTensor._new(rows, cols, fmt, gscale, device, stream)
     if out.rows != rows or out.cols != cols or out.fmt != fmt or out.device != device:
         raise ValueError(f"out must be a microscaled [{rows}, {cols}] matrix of the call's format on x's device")
     if gscale is not None and gscale is not out.gscale:
@@ -608,7 +612,7 @@ def sv_mx_global_scale(x, g=None, stream=None):
     device = x.device
     index = device.index
     if g is None:
-        g = _made(torch.empty(1, dtype=torch.float32, device=device), stream)
+        g = _made(stream, torch.empty, 1, dtype=torch.float32, device=device)
     elif g.dtype != torch.float32 or g.numel() != 1 or g.device != device:
         raise ValueError("g must be a float32 tensor of one value on x's device")
     _call(load().sv_mx_global_scale, index, (x.data_ptr(), x.numel(), _dt(x), g.data_ptr(),
@@ -639,7 +643,7 @@ def sv_mx_dequantize(xq: MxTensor, dtype=torch.bfloat16, y=None, stream=None):
     """The values of a microscaled matrix as [rows, cols] bfloat16 or float32."""
     index = xq.device.index
     if y is None:
-        y = _made(torch.empty(xq.rows, xq.cols, dtype=dtype, device=xq.device), stream)
+        y = _made(stream, torch.empty, xq.rows, xq.cols, dtype=dtype, device=xq.device)
     elif tuple(y.shape) != (xq.rows, xq.cols) or not y.is_contiguous() or y.device != xq.device:
         raise ValueError("y must be a contiguous [rows, cols] tensor on xq's device")
     _call(load().sv_mx_dequantize, index, (xq._ref, y.data_ptr(), _dt(y),
@@ -671,13 +675,13 @@ def sv_rmsnorm(x, w, residual=None, eps: float = 1e-6, fmt: int | None = None, g
         for t in (residual,) if h is None else (residual, h):
             if t is not x and (t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous()):
                 raise ValueError("residual and h must be contiguous tensors of x's shape, dtype and device")
-        h = _made(torch.empty_like(x), stream) if h is None else h
+        h = _made(stream, torch.empty_like, x) if h is None else h
         pr, ph = residual.data_ptr(), h.data_ptr()
     if fmt is None:
         if gscale is not None:
             raise ValueError("gscale goes with fmt=SV_NVFP4")
         if y is None:
-            y = _made(torch.empty_like(x), stream)
+            y = _made(stream, torch.empty_like, x)
         elif y.shape != shape or y.dtype != dtype or y.device != device or not y.is_contiguous():
             raise ValueError("y must be a contiguous tensor of x's shape, dtype and device")
         py, pq = y.data_ptr(), None
@@ -718,7 +722,7 @@ def sv_mx_projection(xq: MxTensor, wq: MxTensor, y=None, ws: Workspace | None = 
     device = xq.device
     index = device.index
     if y is None:
-        y = _made(torch.empty(xq.rows, wq.rows, dtype=torch.bfloat16, device=device), stream)
+        y = _made(stream, torch.empty, xq.rows, wq.rows, dtype=torch.bfloat16, device=device)
     elif (y.dtype != torch.bfloat16 or y.numel() != xq.rows * wq.rows or y.shape[-1] != wq.rows or not y.is_contiguous()
             or y.device != device):
         raise ValueError("y must be a contiguous bfloat16 tensor of x's rows and w's rows on x's device")
@@ -741,7 +745,7 @@ def sv_mx_qkv_projection(xq: MxTensor, wq: MxTensor, B: int, N: int, H: int, D: 
         if t is not None and (t.shape != (B, H, N, D) or t.dtype != torch.bfloat16 or not t.is_contiguous()
                               or t.device != device):
             raise ValueError("q, k, v must be contiguous bfloat16 [B, H, N, D] tensors on x's device")
-    q, k, v = (_made(torch.empty(B, H, N, D, dtype=torch.bfloat16, device=device), stream) if t is None else t
+    q, k, v = (_made(stream, torch.empty, B, H, N, D, dtype=torch.bfloat16, device=device) if t is None else t
                for t in (q, k, v))
     ws = _mx_workspace(ws, device, stream)
     _call(load().sv_mx_qkv_projection, index, (xq._ref, wq._ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), B, N, H, D,
