@@ -159,6 +159,20 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _made(stream, make, *args, **kwargs):
+    """make(*args, **kwargs): a tensor that a call on `stream` (None: the current stream) allocates and writes.
+
+    Its memory belongs to the stream that writes it: memory freed on the current stream may still be read or
+    written there by queued kernels, which a call on another stream does not wait for. The current stream is
+    recorded as one that uses the tensor too, so that it may be read there and dropped without a wait."""
+    if stream is None:
+        return make(*args, **kwargs)
+    with torch.cuda.stream(stream):
+        t = make(*args, **kwargs)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 def _qkv(*ts):
     """Checks q, k, v (and o) in one pass; returns their shape [B, H, N, D]."""
     ref = ts[0]
@@ -193,7 +207,7 @@ class Workspace:
     """
 
     def __init__(self, nbytes: int, device, stream=None):
-        self.buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
+        self.buf = _made(stream, torch.empty, nbytes + 256, dtype=torch.uint8, device=device)
         off = (-self.buf.data_ptr()) % 256
         self.view = self.buf[off:off + nbytes]
         self.nbytes = nbytes
@@ -257,7 +271,7 @@ def _ws(ws, op, q_like, block_len, stream):
 
 def sv_linattn_fwd(q, k, v, o=None, eps: float = 1e-6, ws: Workspace | None = None, stream=None):
     """Bidirectional ReLU linear attention; returns o."""
-    o = torch.empty_like(q) if o is None else o
+    o = _made(stream, torch.empty_like, q) if o is None else o
     B, H, N, D = _qkv(q, k, v, o)
     ws = _ws(ws, SV_OP_LINATTN_FWD, q, None, stream)
     _check(load().sv_linattn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), B, H, N, D, _dt(q), eps, ws.ptr, ws.nbytes,
@@ -268,7 +282,7 @@ def sv_linattn_fwd(q, k, v, o=None, eps: float = 1e-6, ws: Workspace | None = No
 def sv_block_causal_attn(q, k, v, block_len: int, o=None, eps: float = 1e-6, S_in=None, z_in=None, S_out=None,
                          z_out=None, ws: Workspace | None = None, stream=None):
     """Block-causal prefill; returns o (S_out/z_out are written in place when given)."""
-    o = torch.empty_like(q) if o is None else o
+    o = _made(stream, torch.empty_like, q) if o is None else o
     B, H, N, D = _qkv(q, k, v, o)
     for t in (S_in, z_in, S_out, z_out):
         if t is not None and (t.dtype != torch.float32 or not t.is_contiguous() or t.device != q.device):
@@ -283,7 +297,7 @@ def sv_block_causal_attn(q, k, v, block_len: int, o=None, eps: float = 1e-6, S_i
 def sv_cache_step(q, k, v, S, z, commit: bool = True, o=None, eps: float = 1e-6, ws: Workspace | None = None,
                   stream=None):
     """One streaming block against the fp32 cache (S [B,H,D,D], z [B,H,D]); returns o."""
-    o = torch.empty_like(q) if o is None else o
+    o = _made(stream, torch.empty_like, q) if o is None else o
     B, H, N, D = _qkv(q, k, v, o)
     if S.dtype != torch.float32 or z.dtype != torch.float32 or tuple(S.shape) != (B, H, D, D) or tuple(z.shape) != (B, H, D):
         raise ValueError("cache must be float32 S [B,H,D,D] and z [B,H,D]")
@@ -295,7 +309,7 @@ def sv_cache_step(q, k, v, S, z, commit: bool = True, o=None, eps: float = 1e-6,
 
 def sv_cache_step_noalloc(q, k, v, S, z, commit: bool = True, o=None, eps: float = 1e-6, stream=None):
     """sv_cache_step with the library's static scratch instead of a workspace (see the header)."""
-    o = torch.empty_like(q) if o is None else o
+    o = _made(stream, torch.empty_like, q) if o is None else o
     B, H, N, D = _qkv(q, k, v, o)
     if S.dtype != torch.float32 or z.dtype != torch.float32 or tuple(S.shape) != (B, H, D, D) or tuple(z.shape) != (B, H, D):
         raise ValueError("cache must be float32 S [B,H,D,D] and z [B,H,D]")
@@ -347,7 +361,7 @@ def _conv_args(x, w, bias):
 def sv_temporal_conv(x, w, frames_per_block: int, bias=None, y=None, stream=None):
     """Block-causal temporal convolution over x [B, T, S, C] (kernel width 3); returns y."""
     _conv_args(x, w, bias)
-    y = torch.empty_like(x) if y is None else y
+    y = _made(stream, torch.empty_like, x) if y is None else y
     B, T, S, C = x.shape
     _check(load().sv_temporal_conv(_ptr(x), _ptr(y), B, T, S, C, int(frames_per_block), _ptr(w), _ptr(bias), _dt(x),
                                    _stream(stream)))
@@ -361,7 +375,7 @@ def sv_temporal_conv_step(x, w, carry, commit: bool = True, bias=None, y=None, s
     B, T, S, C = x.shape
     if carry.dtype != x.dtype or tuple(carry.shape) != (B, S, C) or not carry.is_contiguous():
         raise ValueError("carry must be a contiguous [B, S, C] tensor of x's dtype")
-    y = torch.empty_like(x) if y is None else y
+    y = _made(stream, torch.empty_like, x) if y is None else y
     _check(load().sv_temporal_conv_step(_ptr(x), _ptr(y), B, T, S, C, _ptr(w), _ptr(bias), _ptr(carry),
                                         1 if commit else 0, _dt(x), _stream(stream)))
     return y
@@ -386,7 +400,8 @@ def sv_qkv_projection(x, w_qkv, H: int, D: int, q=None, k=None, v=None, ws: Work
     B, N, C = x.shape
     if tuple(w_qkv.shape) != (3 * H * D, C) or w_qkv.dtype != torch.bfloat16 or not w_qkv.is_contiguous():
         raise ValueError("w_qkv must be a contiguous bfloat16 [3*H*D, C] tensor")
-    q, k, v = (torch.empty(B, H, N, D, dtype=torch.bfloat16, device=x.device) if t is None else t for t in (q, k, v))
+    q, k, v = (_made(stream, torch.empty, B, H, N, D, dtype=torch.bfloat16, device=x.device) if t is None else t
+               for t in (q, k, v))
     ws = ws if ws is not None else _proj_workspace(x.device, stream)
     _check(load().sv_qkv_projection(_ptr(x), _ptr(w_qkv), _ptr(q), _ptr(k), _ptr(v), B, N, C, H, D, ws.ptr, ws.nbytes,
                                     _stream(stream)))
@@ -401,7 +416,7 @@ def sv_out_projection(o, w_o, y=None, ws: Workspace | None = None, stream=None):
     if w_o.dim() != 2 or w_o.shape[1] != H * D or w_o.dtype != torch.bfloat16 or not w_o.is_contiguous():
         raise ValueError("w_o must be a contiguous bfloat16 [C_out, H*D] tensor")
     C_out = w_o.shape[0]
-    y = torch.empty(B, N, C_out, dtype=torch.bfloat16, device=o.device) if y is None else y
+    y = _made(stream, torch.empty, B, N, C_out, dtype=torch.bfloat16, device=o.device) if y is None else y
     ws = ws if ws is not None else _proj_workspace(o.device, stream)
     _check(load().sv_out_projection(_ptr(o), _ptr(w_o), _ptr(y), B, N, H, D, C_out, ws.ptr, ws.nbytes, _stream(stream)))
     return y
@@ -429,7 +444,7 @@ class Rope3dTable:
                  stream=None):
         pt, ph, pw = (int(p) for p in pairs)
         nbytes = sv_rope3d_table_bytes(frames, height, width, D)
-        self.table = torch.empty(nbytes // 4, dtype=torch.float32, device=device or torch.device("cuda"))
+        self.table = _made(stream, torch.empty, nbytes // 4, dtype=torch.float32, device=device or torch.device("cuda"))
         self.frames, self.height, self.width, self.D, self.pairs = frames, height, width, D, (pt, ph, pw)
         _check(load().sv_rope3d_table(self.table.data_ptr(), nbytes, frames, height, width, D, pt, ph, pw, base,
                                       _stream(stream)))
@@ -447,7 +462,7 @@ def sv_rope3d_table(frames: int, height: int, width: int, D: int, pairs, base: f
 def sv_block_causal_attn_rope(q, k, v, block_len: int, rope: Rope3dTable, frame0: int = 0, o=None, eps: float = 1e-6,
                               S_in=None, z_in=None, S_out=None, z_out=None, ws: Workspace | None = None, stream=None):
     """sv_block_causal_attn with the 3D rotary embedding of the numerator; returns o."""
-    o = torch.empty_like(q) if o is None else o
+    o = _made(stream, torch.empty_like, q) if o is None else o
     B, H, N, D = _qkv(q, k, v, o)
     for t in (S_in, z_in, S_out, z_out):
         if t is not None and (t.dtype != torch.float32 or not t.is_contiguous() or t.device != q.device):
@@ -564,20 +579,6 @@ def _call(fn, index, args):
             st = fn(*args)
     if st != SV_OK:
         _check(st)
-
-
-def _made(stream, make, *args, **kwargs):
-    """make(*args, **kwargs): a tensor that a call on `stream` (None: the current stream) allocates and writes.
-
-    Its memory belongs to the stream that writes it: memory freed on the current stream may still be read or
-    written there by queued kernels, which a call on another stream does not wait for. The current stream is
-    recorded as one that uses the tensor too, so that it may be read there and dropped without a wait."""
-    if stream is None:
-        return make(*args, **kwargs)
-    with torch.cuda.stream(stream):
-        t = make(*args, **kwargs)
-    t.record_stream(torch.cuda.current_stream(t.device))
-    return t
 
 
 def _raw_stream(index):
