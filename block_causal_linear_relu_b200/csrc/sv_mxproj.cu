@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int ta = (ma * g.runs + k0) * C::kTiles;
       int tb = (n0 / 128 * g.runs + k0) * C::kTiles;
       for (int kc = k0; kc < k1; ++kc, ta += C::kTiles, tb += C::kTiles) {
-        if (!warp_all(mbar_wait(&empty[s], phase, status, 0x6100u | s))) {
+        if (!warp_all(mbar_wait_own(&empty[s], phase, status, 0x6100u | s))) {
           ok = false;
           break;
         }
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // the last runs' MMAs report to this CTA's barriers: stay until they have (a slot never used is free)
     for (int i = 0; i < C::kStages && ok; ++i) {
-      ok = warp_all(mbar_wait(&empty[s], phase, status, 0x6180u | s));
+      ok = warp_all(mbar_wait_own(&empty[s], phase, status, 0x6180u | s));
       if (++s == C::kStages) s = 0, phase ^= 1;
     }
   } else if (warp == 1) {  // scales and MMAs
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n0 = (tile % g.nt) * NT;
         const uint32_t shift = static_cast<uint32_t>(n0 % 128) / 32;  // columns of B's first scale block before the tile
         for (int kc = k0; kc < k1; ++kc) {
-          if (!warp_all(ready) && !warp_all(mbar_wait(&full[s], phase, status, 0x6310u | s))) {
+          if (!warp_all(ready) && !warp_all(mbar_wait_own(&full[s], phase, status, 0x6310u | s))) {
             ok = false;
             break;
           }
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           // the accumulator's last tile is drained: asked for after the first run's scales are on their way
           if (kc == k0) {
-            if (!warp_all(mbar_wait(&acce[a], ((tl / C::kAccs) & 1) ^ 1, status, 0x6300u | a))) {
+            if (!warp_all(mbar_wait_own(&acce[a], ((tl / C::kAccs) & 1) ^ 1, status, 0x6300u | a))) {
               ok = false;
               break;
             }
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int tl = 0;
     for (int tile = first; tile < g.tiles; tile += step, ++tl) {
       const int a = tl % C::kAccs;
-      if (!warp_all(mbar_wait(&accf[a], (tl / C::kAccs) & 1, status, 0x6400u | a))) break;
+      if (!warp_all(mbar_wait_own(&accf[a], (tl / C::kAccs) & 1, status, 0x6400u | a))) break;
       tc_fence_after();
       const int m = tile / g.nt, n0 = (tile - m * g.nt) * NT;
       const int row0 = (m * CTAS + rank) * kRows + q * 32;

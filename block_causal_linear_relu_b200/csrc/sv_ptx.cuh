@@ -85,14 +85,18 @@ static __device__ __noinline__ void raise_status(uint32_t* status, uint32_t code
 }
 
 // Slow path of a bounded wait: polls until the phase with `parity` completes, another thread of the
-// grid has raised the status word, or kWaitLimitNs elapse (then it raises SV_DEV_TIMEOUT | where).
+// grid has raised the status word (kShared), or kWaitLimitNs elapse (then it raises SV_DEV_TIMEOUT | where).
+template <bool kShared>
 static __device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity, uint32_t* status,
                                             uint32_t where) {
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((it & 63u) == 0u) {
-      if (*reinterpret_cast<volatile uint32_t*>(status) != 0u) return false;
+      // read in both forms: without the read the callers' registers are laid out anew, and the microscaled
+      // Q/K/V projection spills more of them (1 % slower)
+      const bool raised = *reinterpret_cast<volatile uint32_t*>(status) != 0u;
+      if (kShared && raised) return false;
       if (globaltimer_ns() - t0 > kWaitLimitNs) {
         raise_status(status, kDevTimeout | where);
         return false;
@@ -104,7 +108,15 @@ static __device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parit
 // Returns true once the phase completed; false on timeout or when the grid already failed.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint32_t* status, uint32_t where) {
   if (mbar_try_wait(bar, parity)) return true;
-  return mbar_wait_slow(bar, parity, status, where);
+  return mbar_wait_slow<true>(bar, parity, status, where);
+}
+
+// The same for a kernel that keeps nothing in the workspace but the status word: a word that is raised, by
+// another launch that may run at the same time, does not end the wait. So a role gives up only after
+// kWaitLimitNs of its own waiting, and the copies and MMAs that it issued before have had that long to finish.
+__device__ __forceinline__ bool mbar_wait_own(uint64_t* bar, uint32_t parity, uint32_t* status, uint32_t where) {
+  if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait_slow<false>(bar, parity, status, where);
 }
 
 // ---------------------------------------------------------------------------------------------

@@ -88,7 +88,8 @@ sv_status sv_workspace_init(void* ws, size_t ws_bytes, sv_stream_t stream);
 /* Synchronise `stream`, read the workspace's status word and clear it. SV_OK if no kernel
  * raised it; SV_ERR_TIMEOUT if a bounded wait expired (the word is then in *code, if given).
  * Until it is cleared, a raised word makes every later call on this workspace give up its waits at
- * once (its output is then not written): a timeout is sticky, like a CUDA error. */
+ * once (its output is then not written): a timeout is sticky, like a CUDA error. The microscaled
+ * products keep nothing else in a workspace: they report there, and a raised word does not stop them. */
 sv_status sv_device_status(void* ws, sv_stream_t stream, uint32_t* code);
 
 /* Register a host word that the kernels also write when they raise the workspace's status word, so
@@ -328,7 +329,8 @@ sv_status sv_rmsnorm(const void* x, const void* residual, void* h, const float* 
  * weight (one row per output feature, a multiple of 8). y: DEVICE bf16 [x.rows, w.rows], 16-byte
  * aligned. With x quantised from the attention output this is the output projection. x and w are HOST
  * pointers, read during the call. ws: a workspace of at least 256 bytes (sv_workspace_init), whose
- * status word reports a device-side timeout (sv_device_status). */
+ * status word reports a device-side timeout (sv_device_status); calls that run at the same time, and
+ * captured graphs, may share one. */
 sv_status sv_mx_projection(const sv_mx* x, const sv_mx* w, void* y, void* ws, size_t ws_bytes, sv_stream_t stream);
 
 /* sv_qkv_projection on microscaled operands: x has B * N rows (row b * N + n is token n of batch b), w
