@@ -159,18 +159,22 @@ def _stream(stream):
     return stream.cuda_stream
 
 
-def _made(stream, make, *args, **kwargs):
-    """make(*args, **kwargs): a tensor that a call on `stream` (None: the current stream) allocates and writes.
+def _empty(stream, dtype, device, *shape):
+    """An uninitialised tensor that a call on `stream` (None: the current stream) writes.
 
     Its memory belongs to the stream that writes it: memory freed on the current stream may still be read or
     written there by queued kernels, which a call on another stream does not wait for. The current stream is
     recorded as one that uses the tensor too, so that it may be read there and dropped without a wait."""
     if stream is None:
-        return make(*args, **kwargs)
+        return torch.empty(*shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        t = make(*args, **kwargs)
+        t = torch.empty(*shape, dtype=dtype, device=device)
     t.record_stream(torch.cuda.current_stream(t.device))
     return t
+
+
+def _empty_like(x, stream):
+    return torch.empty_like(x) if stream is None else _empty(stream, x.dtype, x.device, *x.shape)
 
 
 def _qkv(*ts):
@@ -207,7 +211,7 @@ class Workspace:
     """
 
     def __init__(self, nbytes: int, device, stream=None):
-        self.buf = _made(stream, torch.empty, nbytes + 256, dtype=torch.uint8, device=device)
+        self.buf = _empty(stream, torch.uint8, device, nbytes + 256)
         off = (-self.buf.data_ptr()) % 256
         self.view = self.buf[off:off + nbytes]
         self.nbytes = nbytes
@@ -271,7 +275,7 @@ def _ws(ws, op, q_like, block_len, stream):
 
 def sv_linattn_fwd(q, k, v, o=None, eps: float = 1e-6, ws: Workspace | None = None, stream=None):
     """Bidirectional ReLU linear attention; returns o."""
-    o = _made(stream, torch.empty_like, q) if o is None else o
+    o = _empty_like(q, stream) if o is None else o
     B, H, N, D = _qkv(q, k, v, o)
     ws = _ws(ws, SV_OP_LINATTN_FWD, q, None, stream)
     _check(load().sv_linattn_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), B, H, N, D, _dt(q), eps, ws.ptr, ws.nbytes,
@@ -282,7 +286,7 @@ def sv_linattn_fwd(q, k, v, o=None, eps: float = 1e-6, ws: Workspace | None = No
 def sv_block_causal_attn(q, k, v, block_len: int, o=None, eps: float = 1e-6, S_in=None, z_in=None, S_out=None,
                          z_out=None, ws: Workspace | None = None, stream=None):
     """Block-causal prefill; returns o (S_out/z_out are written in place when given)."""
-    o = _made(stream, torch.empty_like, q) if o is None else o
+    o = _empty_like(q, stream) if o is None else o
     B, H, N, D = _qkv(q, k, v, o)
     for t in (S_in, z_in, S_out, z_out):
         if t is not None and (t.dtype != torch.float32 or not t.is_contiguous() or t.device != q.device):
@@ -297,7 +301,7 @@ def sv_block_causal_attn(q, k, v, block_len: int, o=None, eps: float = 1e-6, S_i
 def sv_cache_step(q, k, v, S, z, commit: bool = True, o=None, eps: float = 1e-6, ws: Workspace | None = None,
                   stream=None):
     """One streaming block against the fp32 cache (S [B,H,D,D], z [B,H,D]); returns o."""
-    o = _made(stream, torch.empty_like, q) if o is None else o
+    o = _empty_like(q, stream) if o is None else o
     B, H, N, D = _qkv(q, k, v, o)
     if S.dtype != torch.float32 or z.dtype != torch.float32 or tuple(S.shape) != (B, H, D, D) or tuple(z.shape) != (B, H, D):
         raise ValueError("cache must be float32 S [B,H,D,D] and z [B,H,D]")
@@ -309,7 +313,7 @@ def sv_cache_step(q, k, v, S, z, commit: bool = True, o=None, eps: float = 1e-6,
 
 def sv_cache_step_noalloc(q, k, v, S, z, commit: bool = True, o=None, eps: float = 1e-6, stream=None):
     """sv_cache_step with the library's static scratch instead of a workspace (see the header)."""
-    o = _made(stream, torch.empty_like, q) if o is None else o
+    o = _empty_like(q, stream) if o is None else o
     B, H, N, D = _qkv(q, k, v, o)
     if S.dtype != torch.float32 or z.dtype != torch.float32 or tuple(S.shape) != (B, H, D, D) or tuple(z.shape) != (B, H, D):
         raise ValueError("cache must be float32 S [B,H,D,D] and z [B,H,D]")
@@ -361,7 +365,7 @@ def _conv_args(x, w, bias):
 def sv_temporal_conv(x, w, frames_per_block: int, bias=None, y=None, stream=None):
     """Block-causal temporal convolution over x [B, T, S, C] (kernel width 3); returns y."""
     _conv_args(x, w, bias)
-    y = _made(stream, torch.empty_like, x) if y is None else y
+    y = _empty_like(x, stream) if y is None else y
     B, T, S, C = x.shape
     _check(load().sv_temporal_conv(_ptr(x), _ptr(y), B, T, S, C, int(frames_per_block), _ptr(w), _ptr(bias), _dt(x),
                                    _stream(stream)))
@@ -375,7 +379,7 @@ def sv_temporal_conv_step(x, w, carry, commit: bool = True, bias=None, y=None, s
     B, T, S, C = x.shape
     if carry.dtype != x.dtype or tuple(carry.shape) != (B, S, C) or not carry.is_contiguous():
         raise ValueError("carry must be a contiguous [B, S, C] tensor of x's dtype")
-    y = _made(stream, torch.empty_like, x) if y is None else y
+    y = _empty_like(x, stream) if y is None else y
     _check(load().sv_temporal_conv_step(_ptr(x), _ptr(y), B, T, S, C, _ptr(w), _ptr(bias), _ptr(carry),
                                         1 if commit else 0, _dt(x), _stream(stream)))
     return y
@@ -400,7 +404,7 @@ def sv_qkv_projection(x, w_qkv, H: int, D: int, q=None, k=None, v=None, ws: Work
     B, N, C = x.shape
     if tuple(w_qkv.shape) != (3 * H * D, C) or w_qkv.dtype != torch.bfloat16 or not w_qkv.is_contiguous():
         raise ValueError("w_qkv must be a contiguous bfloat16 [3*H*D, C] tensor")
-    q, k, v = (_made(stream, torch.empty, B, H, N, D, dtype=torch.bfloat16, device=x.device) if t is None else t
+    q, k, v = (_empty(stream, torch.bfloat16, x.device, B, H, N, D) if t is None else t
                for t in (q, k, v))
     ws = ws if ws is not None else _proj_workspace(x.device, stream)
     _check(load().sv_qkv_projection(_ptr(x), _ptr(w_qkv), _ptr(q), _ptr(k), _ptr(v), B, N, C, H, D, ws.ptr, ws.nbytes,
@@ -416,7 +420,7 @@ def sv_out_projection(o, w_o, y=None, ws: Workspace | None = None, stream=None):
     if w_o.dim() != 2 or w_o.shape[1] != H * D or w_o.dtype != torch.bfloat16 or not w_o.is_contiguous():
         raise ValueError("w_o must be a contiguous bfloat16 [C_out, H*D] tensor")
     C_out = w_o.shape[0]
-    y = _made(stream, torch.empty, B, N, C_out, dtype=torch.bfloat16, device=o.device) if y is None else y
+    y = _empty(stream, torch.bfloat16, o.device, B, N, C_out) if y is None else y
     ws = ws if ws is not None else _proj_workspace(o.device, stream)
     _check(load().sv_out_projection(_ptr(o), _ptr(w_o), _ptr(y), B, N, H, D, C_out, ws.ptr, ws.nbytes, _stream(stream)))
     return y
@@ -444,7 +448,7 @@ class Rope3dTable:
                  stream=None):
         pt, ph, pw = (int(p) for p in pairs)
         nbytes = sv_rope3d_table_bytes(frames, height, width, D)
-        self.table = _made(stream, torch.empty, nbytes // 4, dtype=torch.float32, device=device or torch.device("cuda"))
+        self.table = _empty(stream, torch.float32, device or torch.device("cuda"), nbytes // 4)
         self.frames, self.height, self.width, self.D, self.pairs = frames, height, width, D, (pt, ph, pw)
         _check(load().sv_rope3d_table(self.table.data_ptr(), nbytes, frames, height, width, D, pt, ph, pw, base,
                                       _stream(stream)))
@@ -462,7 +466,7 @@ def sv_rope3d_table(frames: int, height: int, width: int, D: int, pairs, base: f
 def sv_block_causal_attn_rope(q, k, v, block_len: int, rope: Rope3dTable, frame0: int = 0, o=None, eps: float = 1e-6,
                               S_in=None, z_in=None, S_out=None, z_out=None, ws: Workspace | None = None, stream=None):
     """sv_block_causal_attn with the 3D rotary embedding of the numerator; returns o."""
-    o = _made(stream, torch.empty_like, q) if o is None else o
+    o = _empty_like(q, stream) if o is None else o
     B, H, N, D = _qkv(q, k, v, o)
     for t in (S_in, z_in, S_out, z_out):
         if t is not None and (t.dtype != torch.float32 or not t.is_contiguous() or t.device != q.device):
@@ -531,7 +535,7 @@ class MxTensor:
         _mx_check(rows, cols, fmt, gscale, device)
         m = cls.__new__(cls)
         n, ns = _mx_sizes(rows, cols, fmt)  # one allocation; codes and scales are views made when asked for
-        m._buf = buf = _made(stream, torch.empty, n + ns, dtype=torch.uint8, device=device)
+        m._buf = buf = _empty(stream, torch.uint8, device, n + ns)
         m._codes = m._scales = None
         m.rows, m.cols, m.fmt, m.gscale, m.device = rows, cols, fmt, gscale, buf.device
         p = buf.data_ptr()
@@ -613,7 +617,7 @@ def sv_mx_global_scale(x, g=None, stream=None):
     device = x.device
     index = device.index
     if g is None:
-        g = _made(stream, torch.empty, 1, dtype=torch.float32, device=device)
+        g = _empty(stream, torch.float32, device, 1)
     elif g.dtype != torch.float32 or g.numel() != 1 or g.device != device:
         raise ValueError("g must be a float32 tensor of one value on x's device")
     _call(load().sv_mx_global_scale, index, (x.data_ptr(), x.numel(), _dt(x), g.data_ptr(),
@@ -644,7 +648,7 @@ def sv_mx_dequantize(xq: MxTensor, dtype=torch.bfloat16, y=None, stream=None):
     """The values of a microscaled matrix as [rows, cols] bfloat16 or float32."""
     index = xq.device.index
     if y is None:
-        y = _made(stream, torch.empty, xq.rows, xq.cols, dtype=dtype, device=xq.device)
+        y = _empty(stream, dtype, xq.device, xq.rows, xq.cols)
     elif tuple(y.shape) != (xq.rows, xq.cols) or not y.is_contiguous() or y.device != xq.device:
         raise ValueError("y must be a contiguous [rows, cols] tensor on xq's device")
     _call(load().sv_mx_dequantize, index, (xq._ref, y.data_ptr(), _dt(y),
@@ -676,13 +680,13 @@ def sv_rmsnorm(x, w, residual=None, eps: float = 1e-6, fmt: int | None = None, g
         for t in (residual,) if h is None else (residual, h):
             if t is not x and (t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous()):
                 raise ValueError("residual and h must be contiguous tensors of x's shape, dtype and device")
-        h = _made(stream, torch.empty_like, x) if h is None else h
+        h = _empty_like(x, stream) if h is None else h
         pr, ph = residual.data_ptr(), h.data_ptr()
     if fmt is None:
         if gscale is not None:
             raise ValueError("gscale goes with fmt=SV_NVFP4")
         if y is None:
-            y = _made(stream, torch.empty_like, x)
+            y = _empty_like(x, stream)
         elif y.shape != shape or y.dtype != dtype or y.device != device or not y.is_contiguous():
             raise ValueError("y must be a contiguous tensor of x's shape, dtype and device")
         py, pq = y.data_ptr(), None
@@ -723,7 +727,7 @@ def sv_mx_projection(xq: MxTensor, wq: MxTensor, y=None, ws: Workspace | None = 
     device = xq.device
     index = device.index
     if y is None:
-        y = _made(stream, torch.empty, xq.rows, wq.rows, dtype=torch.bfloat16, device=device)
+        y = _empty(stream, torch.bfloat16, device, xq.rows, wq.rows)
     elif (y.dtype != torch.bfloat16 or y.numel() != xq.rows * wq.rows or y.shape[-1] != wq.rows or not y.is_contiguous()
             or y.device != device):
         raise ValueError("y must be a contiguous bfloat16 tensor of x's rows and w's rows on x's device")
@@ -746,7 +750,7 @@ def sv_mx_qkv_projection(xq: MxTensor, wq: MxTensor, B: int, N: int, H: int, D: 
         if t is not None and (t.shape != (B, H, N, D) or t.dtype != torch.bfloat16 or not t.is_contiguous()
                               or t.device != device):
             raise ValueError("q, k, v must be contiguous bfloat16 [B, H, N, D] tensors on x's device")
-    q, k, v = (_made(stream, torch.empty, B, H, N, D, dtype=torch.bfloat16, device=device) if t is None else t
+    q, k, v = (_empty(stream, torch.bfloat16, device, B, H, N, D) if t is None else t
                for t in (q, k, v))
     ws = _mx_workspace(ws, device, stream)
     _call(load().sv_mx_qkv_projection, index, (xq._ref, wq._ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), B, N, H, D,
