@@ -698,21 +698,53 @@ def sv_rmsnorm(x, w, residual=None, eps: float = 1e-6, fmt: int | None = None, g
     return y, h
 
 
-_mx_ws = {}
+_mx_ws = {}  # (device index, stream handle): the products' workspace; device index: that of captured calls
+_mx_ws_lock = threading.Lock()
 
 
-def _mx_workspace(ws, device, stream):
-    """The caller's workspace, else the products' own, one per device: they use its status word only, so
-    calls on several streams share it. Raises if an earlier call on it timed out."""
+def _capturing(stream):
+    if torch.cuda.is_current_stream_capturing():
+        return True
+    if stream is None:
+        return False
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
+
+
+def _mx_workspace(ws, device, handle, stream):
+    """The caller's workspace, else one kept per (device, stream), so that a timeout is reported to the stream
+    whose call ran into it. Calls captured on a stream without one share the device's workspace for captures (they
+    use its status word only, and a raised word stops no product); no call sees their replays, so the
+    device's next call reports for them. Raises if an earlier call on the workspace timed out."""
+    if ws is not None:
+        if ws.buf.device != device:
+            raise ValueError("ws must be a workspace on x's device")
+        ws.check(stream)
+        return ws
+    index = device.index
+    ws = _mx_ws.get((index, handle))
     if ws is None:
-        ws = _mx_ws.get(device.index)
-    if ws is None:
-        if torch.cuda.is_current_stream_capturing():
-            raise RuntimeError("the microscaled products' workspace must exist before a capture: make a call first, or pass ws")
-        with torch.cuda.device(device):
-            ws = _mx_ws[device.index] = Workspace(256, device, stream)
-    ws.check(stream)
+        ws = _mx_make_workspace(device, handle, stream)
+    captured = _mx_ws.get(index)
+    if captured is not None and captured._mirror_np[0] != 0:
+        captured.check(stream)
+    if ws._mirror_np[0] != 0:
+        ws.check(stream)
     return ws
+
+
+def _mx_make_workspace(device, handle, stream):
+    index = device.index
+    if _capturing(stream):
+        ws = _mx_ws.get(index)
+        if ws is None:
+            raise RuntimeError("the microscaled products' workspace must exist before a capture: make a call first, or pass ws")
+        return ws
+    with _mx_ws_lock, torch.cuda.device(device):
+        for key in (index, (index, handle)):
+            if key not in _mx_ws:
+                _mx_ws[key] = Workspace(256, device, stream)
+        return _mx_ws[index, handle]
 
 
 def _mx_pair(xq, wq):
@@ -731,9 +763,9 @@ def sv_mx_projection(xq: MxTensor, wq: MxTensor, y=None, ws: Workspace | None = 
     elif (y.dtype != torch.bfloat16 or y.numel() != xq.rows * wq.rows or y.shape[-1] != wq.rows or not y.is_contiguous()
             or y.device != device):
         raise ValueError("y must be a contiguous bfloat16 tensor of x's rows and w's rows on x's device")
-    ws = _mx_workspace(ws, device, stream)
-    _call(load().sv_mx_projection, index, (xq._ref, wq._ref, y.data_ptr(), ws.ptr, ws.nbytes,
-                                           _raw_stream(index) if stream is None else stream.cuda_stream))
+    handle = _raw_stream(index) if stream is None else stream.cuda_stream
+    ws = _mx_workspace(ws, device, handle, stream)
+    _call(load().sv_mx_projection, index, (xq._ref, wq._ref, y.data_ptr(), ws.ptr, ws.nbytes, handle))
     return y
 
 
@@ -752,8 +784,8 @@ def sv_mx_qkv_projection(xq: MxTensor, wq: MxTensor, B: int, N: int, H: int, D: 
             raise ValueError("q, k, v must be contiguous bfloat16 [B, H, N, D] tensors on x's device")
     q, k, v = (_empty(stream, torch.bfloat16, device, B, H, N, D) if t is None else t
                for t in (q, k, v))
-    ws = _mx_workspace(ws, device, stream)
+    handle = _raw_stream(index) if stream is None else stream.cuda_stream
+    ws = _mx_workspace(ws, device, handle, stream)
     _call(load().sv_mx_qkv_projection, index, (xq._ref, wq._ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), B, N, H, D,
-                                               ws.ptr, ws.nbytes,
-                                               _raw_stream(index) if stream is None else stream.cuda_stream))
+                                               ws.ptr, ws.nbytes, handle))
     return q, k, v
