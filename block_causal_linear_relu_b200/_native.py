@@ -659,7 +659,8 @@ def sv_mx_dequantize(xq: MxTensor, dtype=torch.bfloat16, y=None, stream=None):
 def sv_rmsnorm(x, w, residual=None, eps: float = 1e-6, fmt: int | None = None, gscale=None, h=None, y=None, stream=None):
     """Root-mean-square norm over x's last dimension after the residual's addition; returns (y, h).
 
-    h = x + residual in x's dtype (x itself without a residual). y = h / rms(h) * w, in x's dtype and shape,
+    h = x + residual in x's dtype (x itself without a residual; None where y overwrites it, that is, without a
+    residual and with y in x's place). y = h / rms(h) * w, in x's dtype and shape,
     or, with fmt, quantised in the same pass to an MxTensor of one row per position (y, when given, is that
     MxTensor; SV_NVFP4 takes gscale). h may be x or residual (in place)."""
     _dense(x)
@@ -690,6 +691,8 @@ def sv_rmsnorm(x, w, residual=None, eps: float = 1e-6, fmt: int | None = None, g
         elif y.shape != shape or y.dtype != dtype or y.device != device or not y.is_contiguous():
             raise ValueError("y must be a contiguous tensor of x's shape, dtype and device")
         py, pq = y.data_ptr(), None
+        if residual is None and py == x.data_ptr():
+            h = None  # the sum is overwritten
     else:
         y = _mx_out(y, rows, C, fmt, gscale, device, stream)
         py, pq = None, y._ref
