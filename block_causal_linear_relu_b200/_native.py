@@ -502,10 +502,10 @@ class MxTensor:
 
     codes: uint8 [rows, cols] (SV_MXFP8) or [rows, cols / 2]; scales: uint8 [row tiles, block tiles, 32, 4, 4];
     gscale: float32 [1], the tensor scale of SV_NVFP4, None for the other formats. The tensors are read
-    at every call: change them in place, or make another MxTensor.
+    at every call: change them in place, or make another MxTensor (the fields cannot be assigned).
     """
 
-    __slots__ = ("_codes", "_scales", "_buf", "gscale", "rows", "cols", "fmt", "device", "_c", "_ref")
+    __slots__ = ("_codes", "_scales", "_buf", "_gscale", "_rows", "_cols", "_fmt", "_device", "_c", "_ref")
 
     def __init__(self, codes, scales, rows: int, cols: int, fmt: int, gscale=None):
         _mx_check(rows, cols, fmt, gscale, codes.device)
@@ -517,7 +517,7 @@ class MxTensor:
                 or scales.device != codes.device):
             raise ValueError(f"scales must be a contiguous uint8 tensor {_mx_scale_shape(rows, cols, fmt)} on codes' device")
         self._codes, self._scales, self._buf = codes, scales, None
-        self.rows, self.cols, self.fmt, self.gscale, self.device = rows, cols, fmt, gscale, codes.device
+        self._rows, self._cols, self._fmt, self._gscale, self._device = rows, cols, fmt, gscale, codes.device
         self._c = SvMx(codes.data_ptr(), scales.data_ptr(), None if gscale is None else gscale.data_ptr(), rows, cols, fmt)
         self._ref = ctypes.byref(self._c)
 
@@ -537,24 +537,31 @@ class MxTensor:
         n, ns = _mx_sizes(rows, cols, fmt)  # one allocation; codes and scales are views made when asked for
         m._buf = buf = _empty(stream, torch.uint8, device, n + ns)
         m._codes = m._scales = None
-        m.rows, m.cols, m.fmt, m.gscale, m.device = rows, cols, fmt, gscale, buf.device
+        m._rows, m._cols, m._fmt, m._gscale, m._device = rows, cols, fmt, gscale, buf.device
         p = buf.data_ptr()
         m._c = c = SvMx(p, p + n, None if gscale is None else gscale.data_ptr(), rows, cols, fmt)
         m._ref = ctypes.byref(c)
         return m
 
+    # read-only: the descriptor that the calls take holds what they were when it was made
+    rows = property(lambda self: self._rows)
+    cols = property(lambda self: self._cols)
+    fmt = property(lambda self: self._fmt)
+    gscale = property(lambda self: self._gscale)
+    device = property(lambda self: self._device)
+
     @property
     def codes(self):
         if self._codes is None:
-            c = self.cols if self.fmt == SV_MXFP8 else self.cols // 2
-            self._codes = self._buf.as_strided((self.rows, c), (c, 1), 0)
+            c = self._cols if self._fmt == SV_MXFP8 else self._cols // 2
+            self._codes = self._buf.as_strided((self._rows, c), (c, 1), 0)
         return self._codes
 
     @property
     def scales(self):
         if self._scales is None:
-            shape = _mx_scale_shape(self.rows, self.cols, self.fmt)
-            n = _mx_sizes(self.rows, self.cols, self.fmt)[0]
+            shape = _mx_scale_shape(self._rows, self._cols, self._fmt)
+            n = _mx_sizes(self._rows, self._cols, self._fmt)[0]
             self._scales = self._buf.as_strided(shape, (shape[1] * 512, 512, 16, 4, 1), n)
         return self._scales
 
@@ -599,9 +606,9 @@ if hasattr(torch._C, "_cuda_getDevice"):  # the same index; there is a CUDA tens
 def _mx_out(out, rows, cols, fmt, gscale, device, stream):
     if out is None:
         return MxTensor._new(rows, cols, fmt, gscale, device, stream)
-    if out.rows != rows or out.cols != cols or out.fmt != fmt or out.device != device:
+    if out._rows != rows or out._cols != cols or out._fmt != fmt or out._device != device:
         raise ValueError(f"out must be a microscaled [{rows}, {cols}] matrix of the call's format on x's device")
-    if gscale is not None and gscale is not out.gscale:
+    if gscale is not None and gscale is not out._gscale:
         raise ValueError("gscale must be out's own tensor scale, or None")
     return out
 
@@ -646,10 +653,10 @@ def sv_mx_quantize(x, fmt: int, gscale=None, out: MxTensor | None = None, stream
 
 def sv_mx_dequantize(xq: MxTensor, dtype=torch.bfloat16, y=None, stream=None):
     """The values of a microscaled matrix as [rows, cols] bfloat16 or float32."""
-    index = xq.device.index
+    index = xq._device.index
     if y is None:
-        y = _empty(stream, dtype, xq.device, xq.rows, xq.cols)
-    elif tuple(y.shape) != (xq.rows, xq.cols) or not y.is_contiguous() or y.device != xq.device:
+        y = _empty(stream, dtype, xq._device, xq._rows, xq._cols)
+    elif tuple(y.shape) != (xq._rows, xq._cols) or not y.is_contiguous() or y.device != xq._device:
         raise ValueError("y must be a contiguous [rows, cols] tensor on xq's device")
     _call(load().sv_mx_dequantize, index, (xq._ref, y.data_ptr(), _dt(y),
                                            _raw_stream(index) if stream is None else stream.cuda_stream))
@@ -751,7 +758,7 @@ def _mx_make_workspace(device, handle, stream):
 
 
 def _mx_pair(xq, wq):
-    if xq.fmt != wq.fmt or xq.cols != wq.cols or xq.device != wq.device:
+    if xq._fmt != wq._fmt or xq._cols != wq._cols or xq._device != wq._device:
         raise ValueError("x and w must share format, number of columns and device")
 
 
@@ -759,11 +766,11 @@ def sv_mx_projection(xq: MxTensor, wq: MxTensor, y=None, ws: Workspace | None = 
     """y [xq.rows, wq.rows] bfloat16 = x W^T of two microscaled matrices. Make the first call on a device
     (or pass ws) before capturing one into a CUDA graph."""
     _mx_pair(xq, wq)
-    device = xq.device
+    device = xq._device
     index = device.index
     if y is None:
-        y = _empty(stream, torch.bfloat16, device, xq.rows, wq.rows)
-    elif (y.dtype != torch.bfloat16 or y.numel() != xq.rows * wq.rows or y.shape[-1] != wq.rows or not y.is_contiguous()
+        y = _empty(stream, torch.bfloat16, device, xq._rows, wq._rows)
+    elif (y.dtype != torch.bfloat16 or y.numel() != xq._rows * wq._rows or y.shape[-1] != wq._rows or not y.is_contiguous()
             or y.device != device):
         raise ValueError("y must be a contiguous bfloat16 tensor of x's rows and w's rows on x's device")
     handle = _raw_stream(index) if stream is None else stream.cuda_stream
@@ -777,9 +784,9 @@ def sv_mx_qkv_projection(xq: MxTensor, wq: MxTensor, B: int, N: int, H: int, D: 
     """x of B * N rows, w of 3 * H * D rows -> (ReLU(q), ReLU(k), v), each [B, H, N, D] bfloat16. ws as for
     sv_mx_projection."""
     _mx_pair(xq, wq)
-    device = xq.device
+    device = xq._device
     index = device.index
-    if B * N != xq.rows or 3 * H * D != wq.rows:
+    if B * N != xq._rows or 3 * H * D != wq._rows:
         raise ValueError("x must have B * N rows and w 3 * H * D rows")
     for t in (q, k, v):
         if t is not None and (t.shape != (B, H, N, D) or t.dtype != torch.bfloat16 or not t.is_contiguous()

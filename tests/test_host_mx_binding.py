@@ -1,0 +1,30 @@
+"""The binding of the microscaled operators where it needs no GPU: its own checks and fields, on host memory."""
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def native():
+    from block_causal_linear_relu_b200 import _native
+    return _native
+
+
+def matrix(native, rows=3, cols=64, fmt=None, gscale=None):
+    return native.MxTensor._new(rows, cols, native.SV_MXFP8 if fmt is None else fmt, gscale, torch.device("cpu"))
+
+
+def test_fields_cannot_be_assigned(native):
+    # a call reads the descriptor, which would keep the old values and the old tensor scale's address
+    g = torch.ones(1)
+    m = matrix(native, fmt=native.SV_NVFP4, gscale=g)
+    for name, value in (("rows", 5), ("cols", 32), ("fmt", native.SV_MXFP8), ("gscale", torch.zeros(1)), ("device", None),
+                        ("codes", None), ("scales", None)):
+        with pytest.raises(AttributeError):
+            setattr(m, name, value)
+    with pytest.raises(AttributeError):
+        m.other = 1
+    assert (m.rows, m.cols, m.fmt, m.device) == (3, 64, native.SV_NVFP4, torch.device("cpu")) and m.gscale is g
+    assert (m._c.rows, m._c.cols, m._c.fmt, m._c.gscale) == (3, 64, native.SV_NVFP4, g.data_ptr())
+    assert m.codes.shape == (3, 32) and m.codes.data_ptr() == m._c.codes
+    assert m.scales.shape == (1, 4, 32, 4, 4) and m.scales.data_ptr() == m._c.scales
