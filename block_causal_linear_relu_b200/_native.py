@@ -528,6 +528,8 @@ class MxTensor:
             device = gscale.device if gscale is not None else torch.device("cuda", torch.cuda.current_device())
         else:
             device = torch.device(device)
+            if device.type == "cuda" and device.index is None:
+                device = torch.device("cuda", torch.cuda.current_device())
         return cls._new(rows, cols, fmt, gscale, device)
 
     @classmethod

@@ -1,0 +1,27 @@
+"""Arguments of the microscaled calls that are right, or wrong, only on a device."""
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def sv():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a CUDA device")
+    from block_causal_linear_relu_b200 import build
+    build.build()
+    import block_causal_linear_relu_b200 as m
+    m.load()
+    return m
+
+
+@pytest.mark.parametrize("device", ["cuda", torch.device("cuda"), "cuda:0", None])
+def test_empty_takes_a_device_without_an_index(sv, device):
+    g = torch.full((1,), 0.01, device="cuda")
+    x = torch.randn(130, 96, device="cuda")
+    out = sv.MxTensor.empty(130, 96, sv.SV_NVFP4, gscale=g, device=device)
+    assert out.device == x.device
+    assert sv.sv_mx_quantize(x, sv.SV_NVFP4, gscale=g, out=out) is out
+    assert torch.equal(out.codes, sv.sv_mx_quantize(x, sv.SV_NVFP4, gscale=g).codes)
