@@ -715,7 +715,7 @@ sv_status mx_size(sv_mx_format fmt, long long rows, int cols) {
 template <int FMT, typename T>
 sv_status run_quantize(const void* x, int H, int N, int D, const sv_mx& m, int sms, cudaStream_t st) {
   const int sp = mx_padded_blocks(m.fmt, m.cols);
-  const int gp = sp * mx_block(m.fmt) / kGroup;
+  const int gp = sp * (mx_block(m.fmt) / kGroup);  // padded columns may be 2^31
   const long long rows_padded = mx_row_tiles(m.rows) * 128, groups = rows_padded * gp;
   if (groups / (2 * kMxThreads) > 0x7ffffffeLL) return mfail(SV_ERR_UNSUPPORTED, "too many elements");
   const auto go = [&](auto kernel, int steps) {
@@ -779,7 +779,7 @@ sv_status launch_norm(const NormArgs& a, int team, int gp, int sp, cudaStream_t 
 template <int FMT, typename T>
 sv_status run_norm(const NormArgs& a, int sms, cudaStream_t st) {
   const int sp = a.q != nullptr ? mx_padded_blocks(a.q->fmt, a.C) : 0;
-  const int gp = a.q != nullptr ? sp * mx_block(a.q->fmt) / kGroup : (a.C + kOct - 1) / kOct;
+  const int gp = a.q != nullptr ? sp * (mx_block(a.q->fmt) / kGroup) : (a.C + kOct - 1) / kOct;
   // Narrow rows: 8, 16 or 32 lanes each. Few rows: a thread per group of columns, so that a row's latency
   // is one load's and a short sum's. Many: two groups per thread (measured on 55200 x 2560 bf16, plain:
   // 2 groups 164 us, 1 group 215, a warp per row with 10 groups 167; to SV_MXFP8: 166, 180, 348).

@@ -25,3 +25,14 @@ def test_empty_takes_a_device_without_an_index(sv, device):
     assert out.device == x.device
     assert sv.sv_mx_quantize(x, sv.SV_NVFP4, gscale=g, out=out) is out
     assert torch.equal(out.codes, sv.sv_mx_quantize(x, sv.SV_NVFP4, gscale=g).codes)
+
+
+def test_the_widest_rows_are_quantised_whole(sv):
+    cols = 2**31 - 32  # the last group of columns ends below 2^31
+    x = torch.zeros(1, cols, dtype=torch.bfloat16, device="cuda")
+    x[0, -40:] = torch.arange(40, device="cuda").bfloat16() - 20
+    x[0, :32] = 1
+    q = sv.sv_mx_quantize(x, sv.SV_MXFP4)
+    y = sv.sv_mx_dequantize(q)
+    small = sv.sv_mx_dequantize(sv.sv_mx_quantize(x[:, -96:].contiguous(), sv.SV_MXFP4))
+    assert torch.equal(y[:, -96:], small) and bool((y[0, :32] == 1).all()) and not bool(y[0, 32:-96].any())
