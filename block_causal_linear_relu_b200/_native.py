@@ -571,8 +571,8 @@ class MxTensor:
 def _mx_check(rows, cols, fmt, gscale, device):
     if fmt not in (SV_MXFP8, SV_MXFP4, SV_NVFP4):
         raise ValueError("fmt must be SV_MXFP8, SV_MXFP4 or SV_NVFP4")
-    if rows < 1 or cols < 32 or cols % 32 != 0:
-        raise ValueError("rows must be >= 1 and cols a positive multiple of 32")
+    if rows < 1 or not 32 <= cols < 1 << 31 or cols % 32 != 0:  # cols goes to the library as an int
+        raise ValueError("rows must be >= 1 and cols a positive multiple of 32 below 2^31")
     if gscale is None:
         if fmt == SV_NVFP4:
             raise ValueError("SV_NVFP4 needs a tensor scale gscale")
@@ -677,8 +677,8 @@ def sv_rmsnorm(x, w, residual=None, eps: float = 1e-6, fmt: int | None = None, g
     index = device.index
     C = shape[-1] if len(shape) else 0
     rows = x.numel() // C if C else 0
-    if rows == 0:
-        raise ValueError("x must be [..., C] with at least one row and column")
+    if rows == 0 or C > 32768:  # C goes to the library as an int
+        raise ValueError("x must be [..., C] with at least one row and column, and C at most 32768")
     if w.dtype != torch.float32 or w.shape != (C,) or not w.is_contiguous() or w.device != device:
         raise ValueError("w must be a contiguous float32 [C] tensor on x's device")
     if residual is None:

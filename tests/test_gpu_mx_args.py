@@ -27,6 +27,18 @@ def test_empty_takes_a_device_without_an_index(sv, device):
     assert torch.equal(out.codes, sv.sv_mx_quantize(x, sv.SV_NVFP4, gscale=g).codes)
 
 
+def test_columns_past_32_bits_are_refused(sv):
+    # a C int would take 2^32 + 32 columns for 32 of them
+    x = torch.empty(1, 2**32 + 32, dtype=torch.bfloat16, device="cuda")
+    for fmt in (sv.SV_MXFP8, sv.SV_MXFP4):
+        with pytest.raises(ValueError):
+            sv.sv_mx_quantize(x, fmt)
+    with pytest.raises(ValueError):
+        sv.sv_rmsnorm(x, torch.empty(2**32 + 32, device="cuda"))
+    with pytest.raises(ValueError):
+        sv.MxTensor.empty(1, 2**31, sv.SV_MXFP8)
+
+
 def test_the_widest_rows_are_quantised_whole(sv):
     cols = 2**31 - 32  # the last group of columns ends below 2^31
     x = torch.zeros(1, cols, dtype=torch.bfloat16, device="cuda")

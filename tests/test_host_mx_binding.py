@@ -28,3 +28,10 @@ def test_fields_cannot_be_assigned(native):
     assert (m._c.rows, m._c.cols, m._c.fmt, m._c.gscale) == (3, 64, native.SV_NVFP4, g.data_ptr())
     assert m.codes.shape == (3, 32) and m.codes.data_ptr() == m._c.codes
     assert m.scales.shape == (1, 4, 32, 4, 4) and m.scales.data_ptr() == m._c.scales
+
+
+def test_sizes_that_a_c_int_cannot_hold_are_refused(native):
+    for cols in (2**31, 2**32 + 32):
+        with pytest.raises(ValueError):
+            native._mx_check(1, cols, native.SV_MXFP8, None, torch.device("cpu"))
+    native._mx_check(1, 2**31 - 32, native.SV_MXFP8, None, torch.device("cpu"))
