@@ -29,8 +29,7 @@ sv_status fail(sv_status s, const char* fmt, ...) {
   va_start(ap, fmt);
   vsnprintf(buf, sizeof(buf), fmt, ap);
   va_end(ap);
-  g_last_error = buf;
-  return s;
+  return sv::set_last_error(s, buf);
 }
 
 sv_status cuda_fail(cudaError_t e, const char* what) {
@@ -433,6 +432,8 @@ sv_status rope_for(sv::RopeDev& rd, const sv_rope3d* r, int N, int D) {
 
 namespace sv {
 sv_status set_last_error(sv_status status, const char* msg) {
+  // the runtime keeps a failed call's error until it is asked for; the next call here must not find it
+  if (status == SV_ERR_CUDA) (void)cudaGetLastError();
   g_last_error = msg;
   return status;
 }
