@@ -115,7 +115,77 @@ __device__ __forceinline__ __nv_bfloat16* output(const Ops& op, int t) {
   return t == 0 ? op.o0 : (t == 1 ? op.o1 : op.o2);
 }
 
+// The product of the tensor scales as two factors, a sum times `pre` times `post`. A product that leaves fp32's
+// range (g is any positive number) can still give results inside it, and zeros. Sums are zero or between 2^-20
+// and 2^54 in magnitude: with pre near 2^-60 or 2^60 the first step neither rounds to a subnormal nor overflows,
+// and post is a power of two. Ordinary products, within 2^+-60, are `pre` alone, and post is 1.
+struct Alpha {
+  float pre, post;
+};
+__device__ __forceinline__ Alpha tensor_alpha(const Ops& op) {
+  const double g = static_cast<double>(*op.ga) * static_cast<double>(*op.gb);  // exact
+  const int e = static_cast<int>((__double_as_longlong(g) >> 52) & 0x7ff) - 1023;
+  if ((e >= -60 && e <= 60) || e == -1023 || e == 1024) return {static_cast<float>(g), 1.f};  // or zero, infinite, NaN
+  const int s = e > 0 ? e - 60 : e + 60, k = min(max(s, -149), 127);  // past these every sum gives zero, or infinity
+  return {static_cast<float>(g * __longlong_as_double(static_cast<long long>(1023 - s) << 52)),
+          __uint_as_float(k >= -126 ? static_cast<uint32_t>(k + 127) << 23 : 1u << (k + 149))};
+}
+
 __device__ __forceinline__ bool warp_all(bool ok) { return __all_sync(0xffffffffu, ok); }
+
+// Whether a product of the tensor scales, rounded to fp32, may need two factors: outside 2^+-59, or NaN.
+__device__ __forceinline__ bool far(float alpha) { return !(fabsf(alpha) >= 0x1p-59f && fabsf(alpha) <= 0x1p59f); }
+
+// The epilogue of a warp where the tensor scales multiply to a number far from 1: the same results in the
+// plainest way, each lane storing its row. Apart from the other, whose code must not grow: with the second
+// factor's code in its loop the 720p Q/K/V projection took 1 to 4 % longer, although it never ran.
+template <int CTAS, int NT, int kAccs, bool kQKV>
+static __device__ __noinline__ void epilogue_far(Geo g, Ops op, uint32_t tmem, uint64_t* accf, uint64_t* acce,
+                                                 int first, int step, int rank, uint32_t* status) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = warp & 3, half = (warp - 2) >> 2;
+  const Alpha alpha = tensor_alpha(op);
+  int tl = 0;
+  for (int tile = first; tile < g.tiles; tile += step, ++tl) {
+    const int a = tl % kAccs;
+    if (!warp_all(mbar_wait_own(&accf[a], (tl / kAccs) & 1, status, 0x6480u | a))) return;
+    tc_fence_after();
+    const int m = tile / g.nt, n0 = (tile - m * g.nt) * NT;
+    const int row = (m * CTAS + rank) * kRows + q * 32 + lane;
+    const uint32_t ta = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(a * NT);
+#pragma unroll 1
+    for (int c = half; c < NT / 64; c += 2) {
+      uint32_t v[64];
+      tmem_ld_x64(ta + c * 64, v);
+      tmem_wait_ld();
+      const int nc = n0 + c * 64;
+      if (nc < g.nout && row < g.rows) {
+        const Place p = place<kQKV>(g, nc);
+        __nv_bfloat16* const out = output(op, p.t) + offset<kQKV>(g, p, row);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (nc + 8 * j >= g.nout) break;
+          uint32_t w[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const uint32_t* f = v + 8 * j + 2 * u;
+            w[u] = pack_bf16x2(__uint_as_float(f[0]) * alpha.pre * alpha.post, __uint_as_float(f[1]) * alpha.pre * alpha.post);
+            if (kQKV && p.t < 2) w[u] = relu_bf16x2(w[u]);
+          }
+          reinterpret_cast<uint4*>(out)[j] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      __syncwarp();  // the next read of TMEM is the whole warp's
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      if (CTAS == 1)
+        mbar_arrive(&acce[a]);
+      else
+        mbar_arrive_pair(mapa_shared(smem_u32(&acce[a]), 0));
+    }
+  }
+}
 
 template <int FMT, int CTAS, int NT, bool kQKV>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -296,6 +366,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+  } else if (FMT == SV_NVFP4 && (CTAS == 2 || g.split == 1) && far(*op.ga * *op.gb)) {
+    epilogue_far<CTAS, NT, C::kAccs, kQKV>(g, op, tmem, accf, acce, first, step, rank, status);
   } else {  // epilogue: warp w drains TMEM lanes 32 * (w % 4) .. + 31 (rows of this CTA's half)
     const int q = warp & 3, half = (warp - 2) >> 2;
     uint8_t* stg = smem + C::kStagingOff + (warp - 2) * kStaging;
@@ -408,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (CTAS == 1 && g.split > 1) {  // each CTA adds its share of the tile's (row, four columns) items
     const int m = first / g.nt, n0 = (first - m * g.nt) * NT;
     const int rows = min(kRows, g.rows - m * kRows);
-    const float alpha = FMT == SV_NVFP4 ? *op.ga * *op.gb : 1.f;
+    const Alpha alpha = FMT == SV_NVFP4 ? tensor_alpha(op) : Alpha{1.f, 1.f};
     constexpr int kPieces = NT / 4;
     for (int i = krank * kThreads + static_cast<int>(threadIdx.x); i < rows * kPieces; i += g.split * kThreads) {
       const int r = i / kPieces, c4 = i - r * kPieces;  // a warp reads whole rows of a rank: 512 bytes
@@ -425,7 +497,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int nc = n0 + c4 * 4;
       if (nc >= g.nout) continue;
       const Place p = place<kQKV>(g, nc);
-      uint2 w = make_uint2(pack_bf16x2(f[0] * alpha, f[1] * alpha), pack_bf16x2(f[2] * alpha, f[3] * alpha));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] = f[j] * alpha.pre * alpha.post;
+      uint2 w = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
       if (kQKV && p.t < 2) w = make_uint2(relu_bf16x2(w.x), relu_bf16x2(w.y));
       *reinterpret_cast<uint2*>(output(op, p.t) + offset<kQKV>(g, p, m * kRows + r)) = w;
     }
