@@ -36,3 +36,32 @@ def test_in_place_without_a_residual(sv, R, C):
     other = torch.empty_like(x)
     y, h = sv.sv_rmsnorm(x, w, y=other)
     assert h is x and y is other and torch.equal(y, want)
+
+
+# Tolerances as for the norm elsewhere: three fp32 roundings, 3 * 2^-24 relative, one bf16 rounding, 2^-8 at most, and
+# 1e-40 where a product is subnormal.
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("R,C", [(1, 32), (5, 2560), (700, 544), (3, 16384)])
+@pytest.mark.parametrize("size,eps", [(1e-39, 0.0), (1e-41, 0.0), (1e-36, 0.0), (1.2e38, 1e-6), (6e37, 0.0)])
+def test_rows_at_the_ends_of_the_range(sv, dt, R, C, size, eps):
+    gen = torch.Generator("cuda").manual_seed(3)
+    x = (torch.rand(R, C, generator=gen, device="cuda") * 4 - 2).double() * size
+    x[:, 0] = size
+    x = x.to(dt)
+    w = 1 + torch.rand(C, generator=gen, device="cuda")
+    y, _ = sv.sv_rmsnorm(x, w, eps=eps)
+    xd = x.double().cpu().numpy()
+    with np.errstate(invalid="ignore"):
+        ref = M.rms_norm(xd, w.double().cpu().numpy(), float(np.float32(eps)))
+    tol = 3.01 * 2.0**-24 + (2.0**-8 if dt == torch.bfloat16 else 0)
+    y = y.double().cpu().numpy()
+    zero = ~xd.any(axis=1)  # 1e-41 is zero in bf16, and zero rows without an eps are 0 / 0
+    assert np.isfinite(ref[~zero]).all() and np.isnan(y[zero]).all() and np.isnan(ref[zero]).all()
+    assert np.all(np.abs(y - ref)[~zero] <= tol * np.abs(ref[~zero]) + 1e-40)
+    y32, _ = sv.sv_rmsnorm(x.float(), w, eps=eps)
+    for name, fmt in (("mxfp8", sv.SV_MXFP8), ("mxfp4", sv.SV_MXFP4), ("nvfp4", sv.SV_NVFP4)):
+        g = torch.full((1,), 0.002, device="cuda") if name == "nvfp4" else None
+        q, _ = sv.sv_rmsnorm(x, w, eps=eps, fmt=fmt, gscale=g)
+        c, s = M.quantize(y32.double().cpu().numpy(), name, float(g.item()) if g is not None else None)
+        assert np.array_equal(q.scales.cpu().numpy(), M.tile_scales(s, name))
+        assert np.array_equal(M.elements(M.unpack(q.codes.cpu().numpy(), name), name), M.elements(c, name))
