@@ -101,6 +101,13 @@ constexpr int mx_padded_blocks(sv_mx_format f, int cols) {
 }
 // pointers, alignment, sizes and the tensor scale of a microscaled matrix; `name` goes into the message
 sv_status check_mx(const sv_mx* m, const char* name);
+// whether two buffers share bytes (NULL: no buffer)
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a != nullptr && b != nullptr && x < y + nb && y < x + na;
+}
+// whether a buffer shares bytes with the codes or the scales of a microscaled matrix
+bool overlap(const sv_mx& m, const void* p, size_t n);
 // number of SMs of the current device, which must be sm_100 (looked up once per device)
 sv_status mx_device(int* sms);
 // a 2-D byte map [rows, bytes] of codes with boxes of box_rows x 128 bytes, 128-byte swizzle

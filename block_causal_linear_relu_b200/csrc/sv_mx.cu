@@ -733,6 +733,10 @@ sv_status check_dt(sv_dtype dt) {
   return dt == SV_BF16 || dt == SV_F32 ? SV_OK : mfail(SV_ERR_UNSUPPORTED, "dtype is not SV_BF16 or SV_F32");
 }
 
+size_t matrix_bytes(long long rows, int cols, sv_dtype dt) {
+  return static_cast<size_t>(rows) * cols * (dt == SV_F32 ? 4 : 2);
+}
+
 sv_status mx_size(sv_mx_format fmt, long long rows, int cols) {
   if (fmt != SV_MXFP8 && fmt != SV_MXFP4 && fmt != SV_NVFP4)
     return mfail(SV_ERR_UNSUPPORTED, "unknown microscaled format %lld", static_cast<long long>(fmt));
@@ -858,6 +862,11 @@ sv_status check_mx(const sv_mx* m, const char* name) {
   return SV_OK;
 }
 
+bool overlap(const sv_mx& m, const void* p, size_t n) {
+  return overlap(m.codes, sv_mx_code_bytes(m.fmt, m.rows, m.cols), p, n) ||
+         overlap(m.scales, sv_mx_scale_bytes(m.fmt, m.rows, m.cols), p, n);
+}
+
 sv_status mx_device(int* sms) {
   constexpr int kMaxDev = 64;
   static std::mutex mu;
@@ -930,6 +939,8 @@ extern "C" sv_status sv_mx_quantize(const void* x, int B, int H, int N, int D, s
     return mfail(SV_ERR_INVALID_ARG, "out must have B * N = %lld rows and H * D = %lld columns",
                  static_cast<long long>(B) * N, static_cast<long long>(H) * D);
   if (x == nullptr || !aligned(x, 16)) return mfail(SV_ERR_INVALID_ARG, "x must be non-NULL and 16-byte aligned");
+  if (overlap(*out, x, matrix_bytes(out->rows, out->cols, dt)))
+    return mfail(SV_ERR_INVALID_ARG, "out must not overlap x");
   int sms = 0;
   MX_TRY(mx_device(&sms));
   MX_DISPATCH(out->fmt, dt, run_quantize, x, H, N, D, *out, sms, reinterpret_cast<cudaStream_t>(stream));
@@ -940,6 +951,7 @@ extern "C" sv_status sv_mx_dequantize(const sv_mx* in, void* y, sv_dtype dt, sv_
   MX_TRY(check_dt(dt));
   MX_TRY(check_mx(in, "in"));
   if (y == nullptr || !aligned(y, 16)) return mfail(SV_ERR_INVALID_ARG, "y must be non-NULL and 16-byte aligned");
+  if (overlap(*in, y, matrix_bytes(in->rows, in->cols, dt))) return mfail(SV_ERR_INVALID_ARG, "y must not overlap in");
   int sms = 0;
   MX_TRY(mx_device(&sms));
   MX_DISPATCH(in->fmt, dt, run_dequantize, *in, y, reinterpret_cast<cudaStream_t>(stream));
@@ -964,6 +976,15 @@ extern "C" sv_status sv_rmsnorm(const void* x, const void* residual, void* h, co
     if (yq->rows != rows || yq->cols != C)
       return mfail(SV_ERR_INVALID_ARG, "yq must have %lld rows and %lld columns", rows, C);
   }
+  // in place or apart: a row is read before it is written, but not another block's rows
+  const size_t n = matrix_bytes(rows, C, dt);
+  const auto apart = [&](const void* out, const void* in) { return out == in || !overlap(out, n, in, n); };
+  if (!apart(h, x) || !apart(h, residual) || !apart(y, x) || !apart(y, residual) || overlap(y, n, h, n) ||
+      overlap(y, n, w, 4 * static_cast<size_t>(C)) || (residual != nullptr && overlap(h, n, w, 4 * static_cast<size_t>(C))))
+    return mfail(SV_ERR_INVALID_ARG, "y and h must not overlap w, each other, or x or the residual other than in place");
+  if (yq != nullptr && (overlap(*yq, x, n) || overlap(*yq, residual, n) || overlap(*yq, h, n) ||
+                        overlap(*yq, w, 4 * static_cast<size_t>(C))))
+    return mfail(SV_ERR_INVALID_ARG, "yq must not overlap x, residual, h or w");
   int sms = 0;
   MX_TRY(mx_device(&sms));
   // without a residual h is x: nothing to write where they are the same buffer

@@ -660,6 +660,11 @@ sv_status product(const sv_mx& x, const sv_mx& w, const Ops& outs, Geo g, void* 
   if (x.cols != w.cols) return pfail(SV_ERR_INVALID_ARG, "x and w have different columns (%lld and %lld)", x.cols, w.cols);
   if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0u || ws_bytes < static_cast<size_t>(kHeaderBytes))
     return pfail(SV_ERR_INVALID_ARG, "ws must be a 256-byte aligned workspace of at least %lld bytes", kHeaderBytes);
+  const size_t n = 2 * static_cast<size_t>(x.rows) * static_cast<size_t>(kQKV ? w.rows / 3 : w.rows);
+  if (overlap(outs.o0, n, outs.o1, n) || overlap(outs.o0, n, outs.o2, n) || overlap(outs.o1, n, outs.o2, n))
+    return pfail(SV_ERR_INVALID_ARG, "the outputs must not overlap");
+  for (const void* o : {outs.o0, outs.o1, outs.o2})
+    if (overlap(x, o, n) || overlap(w, o, n)) return pfail(SV_ERR_INVALID_ARG, "an output must not overlap x or w");
   g.rows = static_cast<int>(x.rows);
   g.nout = static_cast<int>(w.rows);
   g.runs = mx_runs(x.fmt, x.cols);

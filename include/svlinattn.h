@@ -304,7 +304,8 @@ sv_status sv_mx_global_scale(const void* x, long long n, sv_dtype dt, float* g, 
 /* Quantises x [B, H, N, D] (contiguous, type dt, 16-byte aligned) to the matrix out of B * N rows and
  * H * D columns: row b * N + n holds the heads of token n side by side (the order in which
  * sv_out_projection reads them). H = 1 quantises plain rows. D a multiple of 8, H * D of 32.
- * out (HOST pointer, read during the call) must have rows = B * N and cols = H * D. */
+ * out (HOST pointer, read during the call) must have rows = B * N and cols = H * D. Here and in the other
+ * microscaled calls, outputs that overlap an input or one another are refused, but for sv_rmsnorm in place. */
 sv_status sv_mx_quantize(const void* x, int B, int H, int N, int D, sv_dtype dt, const sv_mx* out, sv_stream_t stream);
 
 /* The values of a microscaled matrix: y [rows, cols] of type dt (16-byte aligned), computed in fp32
