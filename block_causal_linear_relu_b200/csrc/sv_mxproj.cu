@@ -41,6 +41,9 @@ namespace {
 constexpr int kRows = 128;          // rows of A per CTA
 constexpr int kEpiWarps = 8;        // two per 32-lane quarter of TMEM, which share its column chunks
 constexpr int kThreads = 64 + 32 * kEpiWarps;  // warp 0 copies, warp 1 MMAs, then the epilogue
+// A tile's sum has to end before the waits for it do (2 s): 2^26 columns are half a million runs, about 0.4 s where
+// every byte comes from DRAM.
+constexpr int kMaxCols = 1 << 26;
 constexpr int kMaxSplit = 8;        // CTAs that share a tile's K: a portable cluster
 constexpr int kPace = 14;           // sixteenths of the next tile's time that a tile's stores are spread over
 constexpr int kStaging = 32 * 128;  // per epilogue warp: 32 rows x 64 bf16
@@ -658,6 +661,7 @@ template <bool kQKV>
 sv_status product(const sv_mx& x, const sv_mx& w, const Ops& outs, Geo g, void* ws, size_t ws_bytes, cudaStream_t st) {
   if (x.fmt != w.fmt) return pfail(SV_ERR_INVALID_ARG, "x and w have different formats (%lld and %lld)", x.fmt, w.fmt);
   if (x.cols != w.cols) return pfail(SV_ERR_INVALID_ARG, "x and w have different columns (%lld and %lld)", x.cols, w.cols);
+  if (x.cols > kMaxCols) return pfail(SV_ERR_UNSUPPORTED, "cols=%lld must be at most %lld", x.cols, kMaxCols);
   if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0u || ws_bytes < static_cast<size_t>(kHeaderBytes))
     return pfail(SV_ERR_INVALID_ARG, "ws must be a 256-byte aligned workspace of at least %lld bytes", kHeaderBytes);
   const size_t n = 2 * static_cast<size_t>(x.rows) * static_cast<size_t>(kQKV ? w.rows / 3 : w.rows);

@@ -327,7 +327,7 @@ sv_status sv_rmsnorm(const void* x, const void* residual, void* h, const float* 
 /* Product of two microscaled matrices of one format and one number of columns, the linear map
  *     y = x W^T   (y[r][f] = sum_c x[r][c] W[f][c]),
  * on the block-scaled tensor-core path: fp32 accumulation, one bf16 rounding. x: tokens (rows), w:
- * weight (one row per output feature, a multiple of 8). y: DEVICE bf16 [x.rows, w.rows], 16-byte
+ * weight (one row per output feature, a multiple of 8); at most 2^26 columns. y: DEVICE bf16 [x.rows, w.rows], 16-byte
  * aligned. With x quantised from the attention output this is the output projection. x and w are HOST
  * pointers, read during the call. ws: a workspace of at least 256 bytes (sv_workspace_init), whose
  * status word reports a device-side timeout (sv_device_status); calls that run at the same time, and
