@@ -218,6 +218,7 @@ class Workspace:
         self._ptr = self.view.data_ptr()
         self._mirror = torch.zeros(1, dtype=torch.int32).pin_memory()
         self._mirror_np = self._mirror.numpy()
+        self._word = memoryview(self._mirror_np)  # read before every call: a Python int, not a numpy scalar
         lib = load()
         with torch.cuda.device(self.buf.device):
             _check(lib.sv_workspace_init(self._ptr, nbytes, _stream(stream)))
@@ -239,7 +240,7 @@ class Workspace:
     def check(self, stream=None):
         """Raise SvError(SV_ERR_TIMEOUT) if a kernel has reported a timeout on this workspace since the
         last check (reads the host mirror: no synchronisation unless a timeout was reported)."""
-        if self._mirror_np[0] != 0:
+        if self._word[0]:
             code = self.status(stream)
             raise SvError(SV_ERR_TIMEOUT, f"a kernel's bounded wait expired on this workspace "
                                           f"(status word 0x{code:08x}); its output was not written")
@@ -537,7 +538,8 @@ class MxTensor:
         _mx_check(rows, cols, fmt, gscale, device)
         m = cls.__new__(cls)
         n, ns = _mx_sizes(rows, cols, fmt)  # one allocation; codes and scales are views made when asked for
-        m._buf = buf = _empty(stream, torch.uint8, device, n + ns)
+        m._buf = buf = (torch.empty(n + ns, dtype=torch.uint8, device=device) if stream is None
+                        else _empty(stream, torch.uint8, device, n + ns))
         m._codes = m._scales = None
         m._rows, m._cols, m._fmt, m._gscale, m._device = rows, cols, fmt, gscale, buf.device
         p = buf.data_ptr()
@@ -690,7 +692,8 @@ def sv_rmsnorm(x, w, residual=None, eps: float = 1e-6, fmt: int | None = None, g
         for t in (residual,) if h is None else (residual, h):
             if t is not x and (t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous()):
                 raise ValueError("residual and h must be contiguous tensors of x's shape, dtype and device")
-        h = _empty_like(x, stream) if h is None else h
+        if h is None:
+            h = torch.empty_like(x) if stream is None else _empty_like(x, stream)
         pr, ph = residual.data_ptr(), h.data_ptr()
     if fmt is None:
         if gscale is not None:
@@ -737,10 +740,10 @@ def _mx_workspace(ws, device, handle, stream):
     ws = _mx_ws.get((index, handle))
     if ws is None:
         ws = _mx_make_workspace(device, handle, stream)
-    captured = _mx_ws.get(index)
-    if captured is not None and captured._mirror_np[0] != 0:
+    captured = _mx_ws[index]
+    if captured._word[0]:
         captured.check(stream)
-    if ws._mirror_np[0] != 0:
+    if ws._word[0]:
         ws.check(stream)
     return ws
 
@@ -771,7 +774,8 @@ def sv_mx_projection(xq: MxTensor, wq: MxTensor, y=None, ws: Workspace | None = 
     device = xq._device
     index = device.index
     if y is None:
-        y = _empty(stream, torch.bfloat16, device, xq._rows, wq._rows)
+        y = (torch.empty(xq._rows, wq._rows, dtype=torch.bfloat16, device=device) if stream is None
+             else _empty(stream, torch.bfloat16, device, xq._rows, wq._rows))
     elif (y.dtype != torch.bfloat16 or y.numel() != xq._rows * wq._rows or y.shape[-1] != wq._rows or not y.is_contiguous()
             or y.device != device):
         raise ValueError("y must be a contiguous bfloat16 tensor of x's rows and w's rows on x's device")
