@@ -35,3 +35,12 @@ def test_sizes_that_a_c_int_cannot_hold_are_refused(native):
         with pytest.raises(ValueError):
             native._mx_check(1, cols, native.SV_MXFP8, None, torch.device("cpu"))
     native._mx_check(1, 2**31 - 32, native.SV_MXFP8, None, torch.device("cpu"))
+
+
+def test_a_workspace_on_another_device_is_refused(native):
+    # a kernel would read and write its status word through a pointer that its device may not reach
+    class Elsewhere:
+        buf = type("Buffer", (), {"device": torch.device("cuda", 1)})()
+
+    with pytest.raises(ValueError, match="workspace"):
+        native._mx_workspace(Elsewhere(), torch.device("cuda", 0), 0, None)
