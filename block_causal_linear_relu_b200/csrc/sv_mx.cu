@@ -1,8 +1,8 @@
 // Microscaled operands, sm_100a: quantisation to block-scaled 8- and 4-bit floating point, the way
 // back, the tensor scale, and the root-mean-square norm whose output is quantised in the same pass.
 //
-// A pass reads each input once and writes codes and scales once, and HBM bounds all but the quantisation to
-// SV_NVFP4, which its arithmetic bounds. Where a thread quantises it holds 16 consecutive columns, one
+// A pass reads each input once and writes codes and scales once. HBM bounds all but the quantisation, where
+// the issue of instructions does as much, most in SV_NVFP4. Where a thread quantises it holds 16 consecutive columns, one
 // SV_NVFP4 block or half an MX block whose other half is in the neighbouring lane, so that a block's scale
 // is worked out once or twice; elsewhere it holds eight (16 bytes of bf16: coalesced loads and stores).
 //
@@ -422,8 +422,12 @@ struct Walk {
 // A block's threads take kSteps groups each of the (padded row, padded group) grid, kMxThreads apart: rows
 // rounded up to 128 and gp groups per row (a multiple of 8), so every warp is full and the places of the
 // scale tiles that hold no block are written too. Two steps; four, in 64 registers, for bf16 to SV_NVFP4 once
-// they fill the device (20240 x 2560, heads: 30.7 us; two steps 35.1, four in 97 registers 40.2; a block of
-// 2760 rows: 6.7 and 5.7 us). The conversions to e2m1 (8 cycles a pair and warp) bound it there.
+// they fill the device (20240 x 2560, heads: 30 us; two steps 35.1, four in 97 registers 40.2; a block of
+// 2760 rows: 6.7 and 5.7 us). Its instructions bound it there: 73 % of the issue slots and 62 % of the ALU are busy,
+// with 28 warps an SM, DRAM at 42 %. The scale of every 16 columns (two conversions, a reciprocal, four border
+// tests) is what it does beyond SV_MXFP4 (25 us); the conversions to e2m1, 8 cycles a pair and warp, are 5.7 us of
+// either. The bounds on blocks per SM make fp32 to SV_MXFP4 and SV_MXFP8 spill 20 to 36 bytes at 40 registers, and
+// the four steps of SV_NVFP4 36 at 64.
 template <int FMT, typename T, bool kHeads, int kSteps>
 __global__ void __launch_bounds__(kMxThreads, FMT == SV_NVFP4 ? 4 : 6)
     quantize_kernel(const T* __restrict__ x, int H, FastDiv N, FastDiv D, uint32_t rows, int cols, Walk walk, int sp,
@@ -584,8 +588,8 @@ __global__ void __launch_bounds__(kMaxBlock) global_scale_kernel(const T* __rest
 // their uses the 720p prefill took 292 us, bound by their latency). Squares are summed in fp64: then
 // 1 / sqrt(mean + eps), rounded to fp32, does not depend on how the row is split over threads (but for one
 // case in about 1e8), and quantised outputs, where a last-bit difference can move an element by a whole
-// step, do not either. 55200 x 2560 bf16 with a residual: 164 us plain (1.13 GB, 6.9 TB/s: HBM bounds it),
-// 160 us to SV_MXFP8, 166 us to SV_NVFP4.
+// step, do not either. 55200 x 2560 bf16 with a residual: 165 us plain (1.13 GB, 6.9 TB/s: HBM bounds it),
+// 157 us to SV_MXFP8, 161 us to SV_MXFP4, 168 us to SV_NVFP4.
 constexpr int kPlain = -1;
 constexpr int kMaxTeam = 512;
 

@@ -19,10 +19,11 @@
 // drain the accumulator: the tensor scales, bf16, ReLU, a swizzled buffer, and a bulk store of 32 rows x 64
 // columns (row by row where those run into another batch). A tile's rows are consecutive rows of X,
 // whatever batch they belong to, because the scale tiles run over all rows.
-// Measured (20240 x 2560 x 7680): SV_NVFP4 160 us, 4975 TFLOP/s (three quarters of four times the measured
-// bf16 rate), SV_MXFP8 281 us, 2840 TFLOP/s (0.86 of twice it). What bounds the 4-bit kinds is the
-// accumulator's way out of TMEM, which stalls the MMAs (a tile's 5120 MMA cycles take 7400), and long
-// runs of any kind the power limit. One row, 2560 x 2560: 5.7 and 6.0 us.
+// Measured (20240 x 2560 x 7680, plain, in bursts of 3 ms): SV_NVFP4 157 us, 5070 TFLOP/s (0.76 of four times the
+// measured bf16 rate), SV_MXFP4 147, SV_MXFP8 271 us, 2940 TFLOP/s (0.89 of twice it); as the Q/K/V projection 167,
+// 164 and 280 us, whose kernels of 192 and 256 columns spill 24 to 60 bytes at 168 registers. What bounds the
+// 4-bit kinds is the accumulator's way out of TMEM, which stalls the MMAs (a tile's 5120 MMA cycles take 7400), and
+// long runs of any kind the power limit. One row, 2560 x 2560: 4.9 us SV_NVFP4 and SV_MXFP4, 5.7 us SV_MXFP8.
 // Rows past the last one and runs past K are zero-filled by the tensor maps; their scales are zero
 // bytes, which both scale types read as finite numbers.
 #include <cuda.h>
@@ -45,7 +46,9 @@ constexpr int kThreads = 64 + 32 * kEpiWarps;  // warp 0 copies, warp 1 MMAs, th
 // every byte comes from DRAM.
 constexpr int kMaxCols = 1 << 26;
 constexpr int kMaxSplit = 8;        // CTAs that share a tile's K: a portable cluster
-constexpr int kPace = 14;           // sixteenths of the next tile's time that a tile's stores are spread over
+// Sixteenths of the next tile's estimated time that a tile's stores are spread over. Q/K/V of 55200 x 2560, 4 bits: 12
+// takes 3 % longer and 20 up to 6 %; 16 saves 2 % of SV_MXFP4's and costs the plain products 4 %.
+constexpr int kPace = 14;
 constexpr int kStaging = 32 * 128;  // per epilogue warp: 32 rows x 64 bf16
 
 template <int FMT, int CTAS, int NT>
@@ -71,7 +74,8 @@ struct Cfg {
   static constexpr int kAccs = 2 * NT + kStages * kScaleCols <= 512 ? 2 : 1;
   static constexpr uint32_t kScaleCol = kAccs * NT;
   static_assert(kScaleCol + kStages * kScaleCols <= 512, "TMEM columns");
-  // cycles that a run of K takes: 2 per column on the tensor cores, or its bytes at about 60 per cycle
+  // cycles that a run of K takes: 2 per column on the tensor cores, or its bytes at 60 per cycle. An estimate, for
+  // ranking the widths and pacing the stores: loads alone, without MMAs, reach 90 bytes per cycle and SM.
   static constexpr int kRunCycles = 2 * NT > kStageBytes / 60 ? 2 * NT : kStageBytes / 60;
   static constexpr MxKind kKind = FMT == SV_MXFP8 ? kMx8 : FMT == SV_MXFP4 ? kMx4 : kNv4;
 };

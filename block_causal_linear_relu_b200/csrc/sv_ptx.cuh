@@ -1,5 +1,6 @@
 // Thin inline-PTX wrappers for sm_100a: mbarriers with bounded waits, TMA (tensor and plain bulk
-// copies, no cluster multicast anywhere), tcgen05 MMA / TMEM, and proxy fences.
+// copies, none of them multicast: the only multicast is tcgen05.commit's, which signals the barriers of
+// a CTA pair and moves no data), tcgen05 MMA / TMEM, and proxy fences.
 #pragma once
 
 #include <cuda.h>
@@ -241,8 +242,9 @@ __device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
          static_cast<uint64_t>(128 >> 4) << 32 |  // 128 bytes between 8-row groups
          static_cast<uint64_t>(1) << 46;          // descriptor version for sm_100
 }
-// A scale tile from shared memory to four TMEM columns, repeated in the four 32-lane quarters; ordered before the MMAs that this thread issues afterwards. CTAS = 2: each CTA of
-// the pair copies from its own shared memory to its own TMEM, at the same offsets.
+// A scale tile from shared memory to four TMEM columns, repeated in the four 32-lane quarters; ordered before
+// the MMAs that this thread issues afterwards. CTAS = 2: each CTA of the pair copies from its own shared memory
+// to its own TMEM, at the same offsets.
 template <int CTAS>
 __device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint64_t d) {
   if (CTAS == 1)
