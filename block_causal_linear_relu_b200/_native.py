@@ -159,6 +159,13 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _on(stream):
+    """Makes `stream` the current one: a torch stream, or any object with a cuda_stream handle."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream)
+    return torch.cuda.stream(stream)
+
+
 def _empty(stream, dtype, device, *shape):
     """An uninitialised tensor that a call on `stream` (None: the current stream) writes.
 
@@ -167,7 +174,7 @@ def _empty(stream, dtype, device, *shape):
     recorded as one that uses the tensor too, so that it may be read there and dropped without a wait."""
     if stream is None:
         return torch.empty(*shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
+    with _on(stream):
         t = torch.empty(*shape, dtype=dtype, device=device)
     t.record_stream(torch.cuda.current_stream(t.device))
     return t
@@ -722,7 +729,7 @@ def _capturing(stream):
         return True
     if stream is None:
         return False
-    with torch.cuda.stream(stream):
+    with _on(stream):
         return torch.cuda.is_current_stream_capturing()
 
 

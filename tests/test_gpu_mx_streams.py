@@ -85,3 +85,18 @@ def test_outputs_may_be_dropped_while_the_current_stream_reads_them(sv, name):
         trash = [torch.full_like(b, 3) for b in want for _ in range(2)]  # takes what is free on the side stream
     torch.cuda.synchronize()
     assert len(trash) == 2 * len(want) and all(torch.equal(a, b) for a, b in zip(copies, want))
+
+
+@pytest.mark.parametrize("name", ["norm to mxfp8", "tensor scale", "qkv projection"])
+def test_a_stream_may_be_any_object_with_a_handle(sv, name):
+    call = calls(sv)[name]
+    want = [b.clone() for b in buffers(call(None))]
+    side = torch.cuda.Stream()
+
+    class Handle:
+        cuda_stream = side.cuda_stream
+
+    torch.cuda.synchronize()
+    got = call(Handle())
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(buffers(got), want))

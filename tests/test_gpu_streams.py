@@ -88,3 +88,18 @@ def test_a_workspace_does_not_take_memory_that_another_stream_still_uses(sv):
     ws = sv.Workspace(3 << 20, torch.device("cuda:0"), side)
     torch.cuda.synchronize()
     assert ws.status() == 0 and not bool(ws.view[48:].any())  # zero behind the status and mirror words
+
+
+@pytest.mark.parametrize("name", ["linattn_fwd", "temporal_conv", "qkv_projection"])
+def test_a_stream_may_be_any_object_with_a_handle(sv, name):
+    call = calls(sv)[name]
+    want = [t.clone() for t in outputs(call(None))]
+    side = torch.cuda.Stream()
+
+    class Handle:
+        cuda_stream = side.cuda_stream
+
+    torch.cuda.synchronize()
+    got = outputs(call(Handle()))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
