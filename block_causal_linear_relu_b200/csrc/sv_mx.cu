@@ -984,7 +984,8 @@ extern "C" sv_status sv_rmsnorm(const void* x, const void* residual, void* h, co
   const size_t n = matrix_bytes(rows, C, dt);
   const auto apart = [&](const void* out, const void* in) { return out == in || !overlap(out, n, in, n); };
   if (!apart(h, x) || !apart(h, residual) || !apart(y, x) || !apart(y, residual) || overlap(y, n, h, n) ||
-      overlap(y, n, w, 4 * static_cast<size_t>(C)) || (residual != nullptr && overlap(h, n, w, 4 * static_cast<size_t>(C))))
+      overlap(y, n, w, 4 * static_cast<size_t>(C)) ||
+      ((residual != nullptr || h != x) && overlap(h, n, w, 4 * static_cast<size_t>(C))))
     return mfail(SV_ERR_INVALID_ARG, "y and h must not overlap w, each other, or x or the residual other than in place");
   if (yq != nullptr && (overlap(*yq, x, n) || overlap(*yq, residual, n) || overlap(*yq, h, n) ||
                         overlap(*yq, w, 4 * static_cast<size_t>(C))))

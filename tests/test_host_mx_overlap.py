@@ -38,6 +38,7 @@ def test_norm(lib):
         assert refused(lib, f(y=None, yq=mx(MB + at, 6 * MB, rows=4)))
         assert refused(lib, f(y=None, yq=mx(7 * MB, 3 * MB + at, rows=4)))
     assert refused(lib, f(y=4 * MB + 1008)) and refused(lib, f(h=4 * MB + 1008))
+    assert refused(lib, f(res=None, h=4 * MB + 1008))  # h takes a copy of x
     assert refused(lib, f(y=None, yq=mx(MB, 6 * MB, rows=4)))  # quantised in place: other rows' bytes
     for ok in (dict(), dict(h=MB), dict(h=2 * MB), dict(y=MB), dict(y=2 * MB), dict(h=MB + n), dict(y=MB - n), dict(res=MB),
                dict(y=None, yq=mx(MB + n, MB + n + 1024, rows=4))):
