@@ -1,4 +1,4 @@
-"""Products of the most columns that they take: sums of 2^26 terms.
+"""Products of the most columns that they take, sums of 2^26 terms; tensor scales and heads past 32 bits.
 
 Operands are zero but for 16384 places at most. In the MX formats they are powers of two, whose sums fp32 holds
 exactly, so the result has no tolerance. In NVFP4 they stand for 6 * e4m3(a / 6) in place of a: the sums take 16384
@@ -58,3 +58,24 @@ def test_the_longest_sums(sv, fmt, R):
         assert ((y.double() - want).abs() <= (2.0**-8 + 2.0**-9) * want.abs()).all()
     else:
         assert want[-2, 0] == 16384 and want[-1, 0] == 2 * 8192 + 4 and torch.equal(y, want.bfloat16())
+
+
+def test_tensor_scale_and_heads_past_32_bits(sv):
+    # 2.2e9 values: the largest one at either end, and the last rows of a call equal a call on those rows alone
+    B, H, N, D, last = 1, 2, 1_100_003, 1024, 131
+    x = torch.ones(B, H, N, D, dtype=torch.bfloat16, device="cuda")
+    tail = torch.randn(B, H, last, D, generator=torch.Generator("cuda").manual_seed(5), device="cuda").bfloat16()
+    x[:, :, -last:] = tail
+    for at, value in (((0, 0, 0, 0), 2688.0), ((0, 1, N - 1, D - 1), -5376.0), ((0, 1, N // 2, 3), 8064.0)):
+        kept = x[at].item()
+        x[at] = value
+        assert sv.sv_mx_global_scale(x).item() == abs(value) / 2688
+        x[at] = kept
+    g = torch.full((1,), 0.002, device="cuda")
+    for fmt in (sv.SV_MXFP8, sv.SV_NVFP4):
+        gs = g if fmt == sv.SV_NVFP4 else None
+        q = sv.sv_mx_quantize(x, fmt, gscale=gs)
+        part = sv.sv_mx_quantize(tail, fmt, gscale=gs)
+        assert torch.equal(q.codes[-last:], part.codes)
+        r, p = torch.arange(N - last, N), torch.arange(last)
+        assert torch.equal(q.scales[r // 128, :, r % 32, r // 32 % 4], part.scales[p // 128, :, p % 32, p // 32 % 4])
